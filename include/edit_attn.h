@@ -433,6 +433,152 @@ EDIT_API int edit_attn_set_wait_drill(int gn_extra_arrivals, uint64_t limit_ns);
 EDIT_API int edit_linear_attention_noalloc(const void *q, const void *k, const void *v, int B, int N, int M, int C,
                                            int heads, int dtype, float attn_eps, void *out, void *stream);
 
+/* Operators on packed sequences: softmax attention, the gated delta rule and
+ * the norms between them (the notes page has no counterpart: its layers take
+ * rectangular batches with one prompt length; these are the mixers and norms
+ * that text encoders and decoders next to such a layer run on prompts of
+ * different lengths).
+ *
+ * Conventions, on top of those above.
+ *   Rows:     a tensor is [rows][heads][d] (or [rows][C]) with `ld*` elements
+ *             from one row to the next, so that slices of a wider projection
+ *             can be passed as they are; heads and channels are contiguous.
+ *             Sequence s has the rows offsets[s] .. offsets[s + 1] - 1. Rows of
+ *             an output that belong to no sequence are left as they were.
+ *   Offsets:  int32 DEVICE arrays, non-decreasing, inside the rows given. They
+ *             are not read on the host, so a captured call can be replayed with
+ *             other lengths. The kernels clamp whatever they read there to the
+ *             rows given, so that bad values cannot make them read or write
+ *             outside; attention and the delta rule then record EDIT_ERR_SHAPE
+ *             in the workspace's status word (edit_attn_read_status), and the
+ *             results of the call are not to be used. Every call sets the word.
+ *   Head groups: heads is a multiple of kv_heads (or qk_heads); head h reads
+ *             the shared head h / (heads / kv_heads).
+ *   Outputs must not overlap the inputs unless a function says so. Tensors of
+ *   no rows may be NULL. All memory belongs to the current device. */
+
+/* Softmax attention over packed sequences. For row i (0-based) of a sequence
+ * with a query rows and b keys, and per head:
+ *   out_i = sum_j p_ij v_j,  p_i = softmax over the visible j of scale (q_i . k_j),
+ *   visible: j < b, and with `causal` also j <= i + b - a (the last query row
+ *   sees the last key, so that a sequence's newest rows can follow a cache of
+ *   its earlier keys). A row that sees no key (b = 0, or b < a) gets zeros.
+ * q, out [rows_q][heads][d]; k, v [rows_k][kv_heads][d]. Sequence s has the
+ * keys k_offsets[s] .. k_offsets[s + 1] - 1, or, with k_lens, the first
+ * k_lens[s] of them (a cache filled in part; what lies behind is not used,
+ * whatever it holds). k_lens may be NULL. max_k bounds every sequence's key
+ * count (it sizes the split of long key lists over several blocks, joined in a
+ * fixed order; a longer sequence is cut there and recorded as
+ * EDIT_ERR_SHAPE). Scores and sums are fp32; bf16 calls round the weights
+ * p_ij to bf16 before the product with v. A NaN or an infinity in k or v
+ * reaches the rows that see that key and no others.
+ * d a multiple of 8 up to 128, ld* multiples of 8, heads / kv_heads at most 64,
+ * scale positive and finite; else EDIT_ERR_UNSUPPORTED. */
+typedef struct {
+  int dtype; /* edit_dtype of q, k, v, out */
+  int heads, kv_heads, d;
+  int nseq;
+  int causal;
+  int max_k;
+  float scale; /* not defaulted by the library */
+  int64_t rows_q, rows_k;
+  int64_t ldq, ldk, ldv, ldo;
+  const int32_t *q_offsets; /* [nseq + 1] */
+  const int32_t *k_offsets; /* [nseq + 1] */
+  const int32_t *k_lens;    /* [nseq] or NULL */
+  void *workspace; /* device, 256-byte aligned */
+  size_t workspace_bytes;
+} edit_packed_attention;
+
+/* Workspace bytes for calls of at most a->rows_q query rows (0 on an argument
+ * error). Host-only; reads dtype, heads, kv_heads, d, nseq, max_k, rows_q. */
+EDIT_API size_t edit_packed_attention_workspace_bytes(const edit_packed_attention *a);
+EDIT_API int edit_packed_attention_forward(const void *q, const void *k, const void *v,
+                                           const edit_packed_attention *a, void *out, void *stream);
+
+/* The gated delta rule over packed sequences: causal linear attention whose
+ * state decays and, before a token's value is added under its key, gives up
+ * what it held there. Per head, with S [d_k][d_v] (fp32), for each token t:
+ *   S  = exp(g_t) S
+ *   u  = beta_t (v_t - S^T k_t)
+ *   S  = S + k_t u^T
+ *   o_t = scale S^T q_t
+ * q, k [rows][qk_heads][d_k]; v, out [rows][heads][d_v]; g, beta fp32
+ * [rows][heads] with ldg elements between rows (g is a log decay, at most 0;
+ * it is limited below at -200, where exp is 0 in fp32, so that -infinity means
+ * "forget all"). With qk_norm the operator first divides each q_t and k_t by
+ * sqrt(|.|^2 + qk_eps). state_in, state_out fp32 [nseq][heads][d_k][d_v]:
+ * state_in NULL starts from zeros, state_out NULL drops the final states; the
+ * two may be the same buffer (not overlap in another way). A sequence of no rows
+ * copies its state.
+ * d_k a multiple of 8 up to 128, d_v a multiple of 8 up to 256, ldq .. ldo
+ * multiples of 8; else EDIT_ERR_UNSUPPORTED.
+ * edit_delta_rule_step is one token for each of nseq sequences (row s belongs
+ * to sequence s; offsets and rows are not read, no workspace): `state` is
+ * updated in place. */
+typedef struct {
+  int dtype; /* edit_dtype of q, k, v, out */
+  int qk_heads, heads, d_k, d_v;
+  int nseq;
+  int qk_norm;
+  float scale, qk_eps;
+  int64_t rows;
+  int64_t ldq, ldk, ldv, ldo, ldg, ldb; /* ldg: g, ldb: beta */
+  const int32_t *offsets; /* [nseq + 1] */
+  void *workspace; /* device, 256-byte aligned */
+  size_t workspace_bytes;
+} edit_delta_rule;
+
+/* Workspace bytes for calls of at most a->rows rows (0 on an argument error).
+ * Host-only. */
+EDIT_API size_t edit_delta_rule_workspace_bytes(const edit_delta_rule *a);
+EDIT_API int edit_delta_rule_forward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                     const edit_delta_rule *a, const float *state_in, float *state_out, void *out,
+                                     void *stream);
+EDIT_API int edit_delta_rule_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                  const edit_delta_rule *a, float *state, void *out, void *stream);
+
+/* The step between two branches of a block, in one pass: the norm after a
+ * branch, its gate, the residual, and the norm before the next branch.
+ *   r = x + res_scale * act(gate0 + gate[b]) * N_post(y)
+ *   h = N_pre(r) * (1 + scale0 + scale[b]) + shift0 + shift[b]
+ * for each row, b its sample. N_post, N_pre: EDIT_NORM_NONE (identity),
+ * EDIT_NORM_LAYER ((z - mean) / sqrt(var + eps), biased variance) or
+ * EDIT_NORM_RMS (z / sqrt(mean z^2 + eps)), then * w + b with the optional
+ * weights post_w, post_b, pre_w, pre_b [C] (w 1 and b 0 where NULL; not
+ * allowed with EDIT_NORM_NONE). act: EDIT_GATE_LINEAR or EDIT_GATE_TANH.
+ * x, y, r, h [rows][C] with ldx .. ldh; y may be NULL (then r = x, and only h
+ * is formed); r or h may be NULL (not both); r may be x or y and h may be y or
+ * x (same pointer and row stride: each row is read before it is written), and
+ * r and h are two buffers. gate, scale, shift: one vector of C for each sample,
+ * ld_mod elements apart; gate0, scale0, shift0 [C] are common to all samples.
+ * Each of the six may be NULL: missing scale and shift terms count as 0; the
+ * gate is 1 when gate and gate0 are both NULL. Row r belongs to sample s with
+ * offsets[s] <= r < offsets[s + 1] (rows in no sample are left as they were),
+ * or, with offsets NULL, to sample r / rows_per_sample (rows then is at most
+ * samples * rows_per_sample). Sums and norms are fp32 over the unrounded r.
+ * Any C up to 16384 and any strides (16-byte vectors are used where pointers,
+ * strides and C allow). */
+enum { EDIT_NORM_NONE = 0, EDIT_NORM_LAYER = 1, EDIT_NORM_RMS = 2 };
+enum { EDIT_GATE_LINEAR = 0, EDIT_GATE_TANH = 1 };
+
+typedef struct {
+  int dtype; /* edit_dtype of every tensor */
+  int norm_post, norm_pre, gate_act;
+  int C;
+  int samples;
+  float eps, res_scale; /* not defaulted by the library */
+  int64_t rows, rows_per_sample;
+  int64_t ldx, ldy, ldr, ldh, ld_mod;
+  const int32_t *offsets; /* [samples + 1] or NULL */
+  const void *post_w, *post_b, *pre_w, *pre_b;
+  const void *gate0, *scale0, *shift0;
+  const void *gate, *scale, *shift;
+} edit_block_norm;
+
+EDIT_API int edit_block_norm_forward(const void *x, const void *y, const edit_block_norm *a, void *r, void *h,
+                                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

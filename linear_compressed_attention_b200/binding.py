@@ -25,7 +25,9 @@ EXPORTS = ("edit_attn_workspace_bytes", "edit_attn_forward", "mmedit_workspace_b
            "edit_attn_variant_workspace_bytes", "edit_attn_variant_forward", "edit_attn_variant_workspace_layout",
            "edit_attn_set_wait_drill", "edit_attn_band_workspace_bytes", "edit_attn_band_record_bytes",
            "edit_attn_band_partials", "edit_attn_band_finish", "edit_dit_block_workspace_bytes",
-           "edit_dit_block_forward")
+           "edit_dit_block_forward", "edit_packed_attention_workspace_bytes", "edit_packed_attention_forward",
+           "edit_delta_rule_workspace_bytes", "edit_delta_rule_forward", "edit_delta_rule_step",
+           "edit_block_norm_forward")
 STAGE_EVENTS_EDIT, STAGE_EVENTS_MM = 9, 12
 PROC = {"none": 0, "cf": 1, "sc": 2}
 VARIANT_NAMES = ("kcf3_w", "kcf3_b", "kgn_gamma", "kgn_beta", "kcf1_w", "kcf1_b", "o_w", "o_b")
@@ -69,6 +71,33 @@ class EditAttnVariant(ctypes.Structure):
 class WsLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("status", "U", "G", "Q", "KVp", "K", "V", "gn_stats", "Sz", "KT",
                                               "VTx", "Mp", "Wop", "NP")]
+
+
+class PackedAttentionArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "heads", "kv_heads", "d", "nseq", "causal", "max_k")] + \
+               [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("rows_q", "rows_k", "ldq", "ldk", "ldv", "ldo")] + \
+               [(n, ctypes.c_void_p) for n in ("q_offsets", "k_offsets", "k_lens", "workspace")] + \
+               [("workspace_bytes", ctypes.c_size_t)]
+
+
+class DeltaRuleArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "qk_heads", "heads", "d_k", "d_v", "nseq", "qk_norm")] + \
+               [("scale", ctypes.c_float), ("qk_eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("rows", "ldq", "ldk", "ldv", "ldo", "ldg", "ldb")] + \
+               [("offsets", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+NORM = {"none": 0, "layer": 1, "rms": 2}
+GATE_ACT = {"linear": 0, "tanh": 1}
+NORM_VECTORS = ("post_w", "post_b", "pre_w", "pre_b", "gate0", "scale0", "shift0", "gate", "scale", "shift")
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "norm_post", "norm_pre", "gate_act", "C", "samples")] + \
+               [("eps", ctypes.c_float), ("res_scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("rows", "rows_per_sample", "ldx", "ldy", "ldr", "ldh", "ld_mod")] + \
+               [("offsets", ctypes.c_void_p)] + [(n, ctypes.c_void_p) for n in NORM_VECTORS]
 
 
 _lib = None
@@ -119,6 +148,19 @@ def lib():
     L.edit_attn_variant_forward.restype = i
     L.edit_attn_variant_workspace_layout.argtypes = [i, i, i, i, i, W, V, ctypes.POINTER(WsLayout)]
     L.edit_attn_variant_workspace_layout.restype = i
+    PA, DR, BN = (ctypes.POINTER(t) for t in (PackedAttentionArgs, DeltaRuleArgs, BlockNormArgs))
+    L.edit_packed_attention_workspace_bytes.argtypes = [PA]
+    L.edit_packed_attention_workspace_bytes.restype = sz
+    L.edit_packed_attention_forward.argtypes = [p, p, p, PA, p, p]
+    L.edit_packed_attention_forward.restype = i
+    L.edit_delta_rule_workspace_bytes.argtypes = [DR]
+    L.edit_delta_rule_workspace_bytes.restype = sz
+    L.edit_delta_rule_forward.argtypes = [p, p, p, p, p, DR, p, p, p, p]
+    L.edit_delta_rule_forward.restype = i
+    L.edit_delta_rule_step.argtypes = [p, p, p, p, p, DR, p, p, p]
+    L.edit_delta_rule_step.restype = i
+    L.edit_block_norm_forward.argtypes = [p, p, BN, p, p, p]
+    L.edit_block_norm_forward.restype = i
     _lib = L
     return L
 
@@ -451,3 +493,236 @@ class DitBlock:
 
     def status(self, stream=None) -> int:
         return edit_attn_read_status(self.workspace, stream)
+
+
+# ----------------------------------------------------------- packed sequences
+def edit_packed_attention_workspace_bytes(args: PackedAttentionArgs) -> int:
+    return int(lib().edit_packed_attention_workspace_bytes(ctypes.byref(args)))
+
+
+def edit_packed_attention_forward(q, k, v, args: PackedAttentionArgs, out, stream=None) -> int:
+    return int(lib().edit_packed_attention_forward(_ptr(q), _ptr(k), _ptr(v), ctypes.byref(args), _ptr(out),
+                                                   _stream(stream)))
+
+
+def edit_delta_rule_workspace_bytes(args: DeltaRuleArgs) -> int:
+    return int(lib().edit_delta_rule_workspace_bytes(ctypes.byref(args)))
+
+
+def edit_delta_rule_forward(q, k, v, g, beta, args: DeltaRuleArgs, state_in, state_out, out, stream=None) -> int:
+    return int(lib().edit_delta_rule_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.byref(args),
+                                             _ptr(state_in), _ptr(state_out), _ptr(out), _stream(stream)))
+
+
+def edit_delta_rule_step(q, k, v, g, beta, args: DeltaRuleArgs, state, out, stream=None) -> int:
+    return int(lib().edit_delta_rule_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.byref(args),
+                                          _ptr(state), _ptr(out), _stream(stream)))
+
+
+def edit_block_norm_forward(x, y, args: BlockNormArgs, r_out, h_out, stream=None) -> int:
+    return int(lib().edit_block_norm_forward(_ptr(x), _ptr(y), ctypes.byref(args), _ptr(r_out), _ptr(h_out),
+                                             _stream(stream)))
+
+
+def _check_rows(name, t, dtype, shape, device):
+    """A device tensor of rows whose other dimensions are contiguous; returns its row stride."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is not on the current device")
+    st = t.stride()
+    if shape[0] == 0:
+        return int(np.prod(shape[1:]))
+    if st[-1] != 1 and shape[-1] > 1 or (len(st) == 3 and st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: only the rows may be strided")
+    return st[0] if shape[0] > 1 else int(np.prod(shape[1:]))
+
+
+def _check_ints(name, t, n, device):
+    import torch
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: {n} contiguous int32 on the current device expected")
+    return t.data_ptr()
+
+
+class _Packed:
+    def __init__(self, dtype):
+        import torch
+        self.torch = torch
+        self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.code = EDIT_BF16 if dtype == "bf16" else EDIT_F32
+
+    def _workspace(self, nbytes, device):
+        if nbytes == 0:
+            raise ValueError("shape/dtype rejected by the workspace query")
+        self.workspace = self.torch.empty(nbytes, dtype=self.torch.uint8, device=device)
+        self.args.workspace, self.args.workspace_bytes = self.workspace.data_ptr(), nbytes
+
+    def status(self, stream=None) -> int:
+        """The last call's device-side status (EDIT_ERR_SHAPE: offsets or lengths out of range); waits for it."""
+        return edit_attn_read_status(self.workspace, stream)
+
+
+class PackedAttention(_Packed):
+    """Softmax attention over packed sequences, with its workspace: up to
+    ``max_rows`` query rows of ``nseq`` sequences with at most ``max_k`` keys
+    each. Calls that may overlap on the GPU need objects of their own."""
+
+    def __init__(self, heads: int, kv_heads: int, d: int, nseq: int, max_rows: int, max_k: int, dtype: str = "bf16",
+                 causal: bool = False, scale: float | None = None, device="cuda"):
+        super().__init__(dtype)
+        a = self.args = PackedAttentionArgs()
+        a.dtype, a.heads, a.kv_heads, a.d, a.nseq, a.causal, a.max_k = \
+            self.code, heads, kv_heads, d, nseq, int(causal), max_k
+        a.scale = d ** -0.5 if scale is None else scale
+        a.rows_q = max_rows
+        self._workspace(edit_packed_attention_workspace_bytes(a), device)
+
+    def forward(self, q, k, v, q_offsets, k_offsets, k_lens=None, out=None, stream=None):
+        """q [rows, heads, d], k, v [rows, kv_heads, d]; int32 device offsets [nseq + 1] and lengths [nseq]."""
+        a, dev = self.args, self.torch.cuda.current_device()
+        rk = k.shape[0]
+        a.rows_q, a.rows_k = q.shape[0], rk
+        a.ldq = _check_rows("q", q, self.tdtype, (a.rows_q, a.heads, a.d), dev)
+        a.ldk = _check_rows("k", k, self.tdtype, (rk, a.kv_heads, a.d), dev)
+        a.ldv = _check_rows("v", v, self.tdtype, (rk, a.kv_heads, a.d), dev)
+        if out is None:
+            out = self.torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        a.ldo = _check_rows("out", out, self.tdtype, (a.rows_q, a.heads, a.d), dev)
+        a.q_offsets = _check_ints("q_offsets", q_offsets, a.nseq + 1, dev)
+        a.k_offsets = _check_ints("k_offsets", k_offsets, a.nseq + 1, dev)
+        a.k_lens = None if k_lens is None else _check_ints("k_lens", k_lens, a.nseq, dev)
+        rc = edit_packed_attention_forward(q, k, v, a, out, stream)
+        if rc != 0:
+            raise EditError(rc)
+        return out
+
+
+class DeltaRule(_Packed):
+    """The gated delta rule for ``nseq`` sequences, with the workspace of calls
+    of up to ``max_rows`` packed rows (``forward``) and the single-token form
+    (``step``). Calls that may overlap on the GPU need objects of their own."""
+
+    def __init__(self, qk_heads: int, heads: int, d_k: int, d_v: int, nseq: int, max_rows: int, dtype: str = "bf16",
+                 scale: float | None = None, qk_norm: bool = True, qk_eps: float = 1e-6, device="cuda"):
+        super().__init__(dtype)
+        a = self.args = DeltaRuleArgs()
+        a.dtype, a.qk_heads, a.heads, a.d_k, a.d_v, a.nseq, a.qk_norm = \
+            self.code, qk_heads, heads, d_k, d_v, nseq, int(qk_norm)
+        a.scale, a.qk_eps = d_k ** -0.5 if scale is None else scale, qk_eps
+        a.rows = max_rows
+        self.state_shape = (nseq, heads, d_k, d_v)
+        self._workspace(edit_delta_rule_workspace_bytes(a), device)
+
+    def _inputs(self, q, k, v, g, beta, out):
+        a, dev, f32 = self.args, self.torch.cuda.current_device(), self.torch.float32
+        n = q.shape[0]
+        a.ldq = _check_rows("q", q, self.tdtype, (n, a.qk_heads, a.d_k), dev)
+        a.ldk = _check_rows("k", k, self.tdtype, (n, a.qk_heads, a.d_k), dev)
+        a.ldv = _check_rows("v", v, self.tdtype, (n, a.heads, a.d_v), dev)
+        a.ldg = _check_rows("g", g, f32, (n, a.heads), dev)
+        a.ldb = _check_rows("beta", beta, f32, (n, a.heads), dev)
+        if out is None:
+            out = self.torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        a.ldo = _check_rows("out", out, self.tdtype, (n, a.heads, a.d_v), dev)
+        return n, dev, out
+
+    def _state(self, name, t, dev):
+        if t is not None and (t.dtype != self.torch.float32 or tuple(t.shape) != self.state_shape or
+                              not t.is_contiguous() or t.get_device() != dev):
+            raise ValueError(f"{name}: contiguous float32 {self.state_shape} on the current device expected")
+
+    def forward(self, q, k, v, g, beta, offsets, state_in=None, state_out=None, out=None, stream=None):
+        """q, k [rows, qk_heads, d_k], v [rows, heads, d_v], fp32 g, beta [rows, heads]; int32 device offsets
+        [nseq + 1]. state_out (which may be state_in) takes the final states. Returns out."""
+        n, dev, out = self._inputs(q, k, v, g, beta, out)
+        a = self.args
+        a.rows = n
+        a.offsets = _check_ints("offsets", offsets, a.nseq + 1, dev)
+        self._state("state_in", state_in, dev)
+        self._state("state_out", state_out, dev)
+        rc = edit_delta_rule_forward(q, k, v, g, beta, a, state_in, state_out, out, stream)
+        if rc != 0:
+            raise EditError(rc)
+        return out
+
+    def step(self, q, k, v, g, beta, state, out=None, stream=None):
+        """One token of each sequence (row s: sequence s); state is updated in place. Returns out."""
+        n, dev, out = self._inputs(q, k, v, g, beta, out)
+        a = self.args
+        if n != a.nseq:
+            raise ValueError(f"{a.nseq} rows expected, one a sequence")
+        self._state("state", state, dev)
+        rc = edit_delta_rule_step(q, k, v, g, beta, a, state, out, stream)
+        if rc != 0:
+            raise EditError(rc)
+        return out
+
+
+class BlockNorm:
+    """The step between two branches of a block: r = x + res_scale act(gate)
+    N_post(y), h = N_pre(r) (1 + scale) + shift, with the weights and common
+    vectors ([C] device tensors, or None) that a layer keeps."""
+
+    def __init__(self, C: int, dtype: str = "bf16", post: str = "none", pre: str = "layer", gate_act: str = "linear",
+                 eps: float = 1e-6, res_scale: float = 1.0, post_w=None, post_b=None, pre_w=None, pre_b=None,
+                 gate0=None, scale0=None, shift0=None):
+        import torch
+        self.torch = torch
+        self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        a = self.args = BlockNormArgs()
+        a.dtype = EDIT_BF16 if dtype == "bf16" else EDIT_F32
+        a.norm_post, a.norm_pre, a.gate_act, a.C = NORM[post], NORM[pre], GATE_ACT[gate_act], C
+        a.eps, a.res_scale = eps, res_scale
+        self.kept = dict(post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b, gate0=gate0, scale0=scale0,
+                         shift0=shift0)
+        for n, t in self.kept.items():
+            if t is not None:
+                if t.dtype != self.tdtype or tuple(t.shape) != (C,) or not t.is_contiguous() or not t.is_cuda:
+                    raise ValueError(f"{n}: contiguous {self.tdtype} ({C},) on the device expected")
+                setattr(a, n, t.data_ptr())
+
+    def forward(self, x, y=None, gate=None, scale=None, shift=None, offsets=None, r_out=None, h_out=None,
+                want_r: bool = True, want_h: bool = True, stream=None):
+        """x, y [rows, C]; gate, scale, shift [samples, C] with one row stride; int32 device offsets [samples + 1],
+        or equal shares of the rows without them. Returns (r, h), None for one that is not wanted."""
+        a, dev = self.args, self.torch.cuda.current_device()
+        n, C = x.shape[0], a.C
+        a.rows = n
+        a.ldx = _check_rows("x", x, self.tdtype, (n, C), dev)
+        if y is not None:
+            a.ldy = _check_rows("y", y, self.tdtype, (n, C), dev)
+        samples, strides = None, set()
+        for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+            if t is None:
+                setattr(a, name, None)
+                continue
+            samples = t.shape[0] if samples is None else samples
+            strides.add(_check_rows(name, t, self.tdtype, (samples, C), dev))
+            setattr(a, name, t.data_ptr())
+        if len(strides) > 1:
+            raise ValueError("gate, scale and shift: one row stride expected")
+        if strides:
+            a.ld_mod = strides.pop()
+        if offsets is not None:
+            samples = offsets.numel() - 1 if samples is None else samples
+            a.offsets = _check_ints("offsets", offsets, samples + 1, dev)
+        else:
+            a.offsets = None
+            samples = samples or 1
+            if samples < 1 or n % samples:
+                raise ValueError("rows do not divide into the samples: give offsets")
+            a.rows_per_sample = max(1, n // samples)
+        a.samples = samples
+        if r_out is None and want_r:
+            r_out = self.torch.empty((n, C), dtype=x.dtype, device=x.device)
+        if h_out is None and want_h:
+            h_out = self.torch.empty((n, C), dtype=x.dtype, device=x.device)
+        if r_out is not None:
+            a.ldr = _check_rows("r_out", r_out, self.tdtype, (n, C), dev)
+        if h_out is not None:
+            a.ldh = _check_rows("h_out", h_out, self.tdtype, (n, C), dev)
+        rc = edit_block_norm_forward(x, y, a, r_out, h_out, stream)
+        if rc != 0:
+            raise EditError(rc)
+        return r_out, h_out

@@ -7,15 +7,17 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", "edit_attn.cu"), os.path.join(PKG, "csrc", "edit_noalloc.cu")]
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("edit_attn.cu", "edit_noalloc.cu", "packed_ops.cu")]
 OUT = os.path.join(PKG, "libedit_attn.so")
 DEPS = [os.path.join(PKG, "csrc", f) for f in ("edit_attn.cu", "edit_noalloc.cu", "common.cuh", "tc_gemm.cuh",
-                                                "tc_conv.cuh", "simt_kernels.cuh", "sdpa_tc.cuh")]
+                                                "tc_conv.cuh", "simt_kernels.cuh", "sdpa_tc.cuh", "packed_ops.cu",
+                                                "host.h", "packed_seq.cuh", "packed_attn.cuh", "delta_rule.cuh",
+                                                "block_norm.cuh")]
 DEPS.append(os.path.join(ROOT, "include", "edit_attn.h"))
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-              "-diag-suppress", "177"]
+              "-diag-suppress", "177", "--threads", "0"]
 
 
 def nvcc():

@@ -25,6 +25,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "host.h"
 #include "sdpa_tc.cuh"
 #include "simt_kernels.cuh"
 #include "tc_conv.cuh"
@@ -1923,6 +1924,11 @@ int common_checks(const void* x, const void* out, const edit_attn_weights* w, vo
 }
 
 }  // namespace
+
+namespace edit {
+void count_launch() { ++g_launches; }
+int device_sms() { return num_sms(); }
+}  // namespace edit
 
 // =================================================================== C ABI
 extern "C" {

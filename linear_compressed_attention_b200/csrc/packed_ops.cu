@@ -1,0 +1,376 @@
+// C ABI of the packed-sequence operators (include/edit_attn.h): argument
+// checks, launch rules and workspace plans of the packed softmax attention, the
+// gated delta rule and the block norm.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+#include <utility>
+
+#include "block_norm.cuh"
+#include "common.cuh"
+#include "delta_rule.cuh"
+#include "host.h"
+#include "packed_attn.cuh"
+
+using namespace edit;
+
+namespace {
+
+#define EDIT_TRY(expr)              \
+  do {                              \
+    const int rc_ = (expr);         \
+    if (rc_ != EDIT_OK) return rc_; \
+  } while (0)
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+
+// One kernel on `st`, with programmatic stream serialization as every kernel of
+// the library; counted for edit_attn_kernel_launches.
+template <typename... KArgs, typename... Args>
+int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return EDIT_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? EDIT_OK : EDIT_ERR_CUDA;
+}
+
+// Leading dimension of rows of `width` values: wide enough, rows 16-byte
+// aligned for the vector accesses (8 elements cover both dtypes).
+int check_ld(int64_t ld, int64_t width) {
+  if (ld < width) return EDIT_ERR_SHAPE;
+  return ld % 8 == 0 ? EDIT_OK : EDIT_ERR_UNSUPPORTED;
+}
+
+// ------------------------------------------------------------ packed attention
+constexpr size_t kStatusBytes = 256;
+
+struct AttnPlan {
+  int R;  // tokens of a row tile
+  int slots, nsplit;
+  size_t part_o, part_ml, total;
+};
+
+int attn_rows(int dtype, int G) { return 64 / G; }
+
+int attn_args(const edit_packed_attention* a) {
+  if (!a) return EDIT_ERR_NULL;
+  if (a->dtype != EDIT_F32 && a->dtype != EDIT_BF16) return EDIT_ERR_DTYPE;
+  if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0 || a->d < 1 || a->nseq < 1 || a->max_k < 0 ||
+      a->rows_q < 0 || a->rows_k < 0)
+    return EDIT_ERR_SHAPE;
+  if (a->d % 8 != 0 || a->d > 128 || a->heads / a->kv_heads > 64 || a->kv_heads > 65535) return EDIT_ERR_UNSUPPORTED;
+  if (a->rows_q > INT32_MAX || a->rows_k > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (a->rows_q / attn_rows(a->dtype, a->heads / a->kv_heads) + a->nseq > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  return EDIT_OK;
+}
+
+// Parts of the key lists when there are `slots` row tiles for each key/value
+// head: enough blocks for every SM, at least 256 keys a part.
+int attn_nsplit(long slots, const edit_packed_attention* a, int sms) {
+  const long want = sms / (slots * a->kv_heads), most = ceil_div(a->max_k, 256);
+  const long n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+void attn_plan(const edit_packed_attention* a, int64_t rows, AttnPlan& pl) {
+  pl.R = attn_rows(a->dtype, a->heads / a->kv_heads);
+  pl.slots = static_cast<int>(rows / pl.R + a->nseq);
+  pl.nsplit = rows > 0 ? attn_nsplit(pl.slots, a, device_sms()) : 1;
+  const size_t items = static_cast<size_t>(pl.nsplit) * rows * a->heads;
+  pl.part_o = kStatusBytes;
+  pl.part_ml = pl.part_o + (pl.nsplit > 1 ? align256(items * a->d * 4) : 0);
+  pl.total = pl.part_ml + (pl.nsplit > 1 ? align256(items * 8) : 0);
+}
+
+template <typename T, int DP>
+int attn_simt(const PackedAttnParams& p, cudaStream_t st) {
+  const size_t smem = (2 * 64 * (DP + 4) + 64 * DP + 64 * 68) * sizeof(float);
+  return launch(packed_attn_simt_kernel<T, DP>, dim3(p.slots, p.kv_heads, p.nsplit), dim3(256), smem, st, p);
+}
+
+template <typename T>
+int attn_run(const PackedAttnParams& p, cudaStream_t st) {
+  EDIT_TRY(p.d <= 64 ? (attn_simt<T, 64>(p, st)) : (attn_simt<T, 128>(p, st)));
+  if (p.nsplit == 1) return EDIT_OK;
+  return launch(packed_attn_join_kernel<T>, dim3(static_cast<unsigned>(ceil_div(static_cast<long>(p.rows_q) * p.heads, 4))),
+                dim3(128), 0, st, p);
+}
+
+// ------------------------------------------------------------ delta rule
+int delta_args(const edit_delta_rule* a, bool step) {
+  if (!a) return EDIT_ERR_NULL;
+  if (a->dtype != EDIT_F32 && a->dtype != EDIT_BF16) return EDIT_ERR_DTYPE;
+  if (a->qk_heads < 1 || a->heads < 1 || a->heads % a->qk_heads != 0 || a->d_k < 1 || a->d_v < 1 || a->nseq < 1 ||
+      (!step && a->rows < 0))
+    return EDIT_ERR_SHAPE;
+  if (a->d_k % 8 != 0 || a->d_k > 128 || a->d_v % 8 != 0 || a->d_v > 256 || a->heads > 65535)
+    return EDIT_ERR_UNSUPPORTED;
+  if (!step && a->rows > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (static_cast<long>(a->nseq) * 4 > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  return EDIT_OK;
+}
+
+int delta_call(const void* q, const void* k, const void* v, const float* g, const float* beta,
+               const edit_delta_rule* a, int64_t rows, const void* out) {
+  if (rows > 0 && (!q || !k || !v || !g || !beta || !out)) return EDIT_ERR_NULL;
+  EDIT_TRY(check_ld(a->ldq, static_cast<int64_t>(a->qk_heads) * a->d_k));
+  EDIT_TRY(check_ld(a->ldk, static_cast<int64_t>(a->qk_heads) * a->d_k));
+  EDIT_TRY(check_ld(a->ldv, static_cast<int64_t>(a->heads) * a->d_v));
+  EDIT_TRY(check_ld(a->ldo, static_cast<int64_t>(a->heads) * a->d_v));
+  if (a->ldg < a->heads || a->ldb < a->heads) return EDIT_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(g, 4) ||
+      !aligned(beta, 4))
+    return EDIT_ERR_ALIGN;
+  return EDIT_OK;
+}
+
+DeltaParams delta_params(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                         const edit_delta_rule* a, void* out) {
+  DeltaParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = g;
+  p.beta = beta;
+  p.out = out;
+  p.rows = a->rows;
+  p.ldq = a->ldq;
+  p.ldk = a->ldk;
+  p.ldv = a->ldv;
+  p.ldo = a->ldo;
+  p.ldg = a->ldg;
+  p.ldb = a->ldb;
+  p.qk_heads = a->qk_heads;
+  p.heads = a->heads;
+  p.d_k = a->d_k;
+  p.d_v = a->d_v;
+  p.nseq = a->nseq;
+  p.qk_norm = a->qk_norm;
+  p.scale = a->scale;
+  p.qk_eps = a->qk_eps;
+  return p;
+}
+
+template <typename T>
+int delta_recurrent(const DeltaParams& p, cudaStream_t st) {
+  const int cb = static_cast<int>(ceil_div(p.d_v, 64));
+  const dim3 grid(static_cast<unsigned>(p.nseq) * cb, p.heads), block(128);
+  if (p.d_k <= 32) return launch(delta_recurrent_kernel<T, 32>, grid, block, 0, st, p, cb);
+  if (p.d_k <= 64) return launch(delta_recurrent_kernel<T, 64>, grid, block, 0, st, p, cb);
+  if (p.d_k <= 96) return launch(delta_recurrent_kernel<T, 96>, grid, block, 0, st, p, cb);
+  return launch(delta_recurrent_kernel<T, 128>, grid, block, 0, st, p, cb);
+}
+
+// ------------------------------------------------------------ block norm
+template <typename T, int VEC, int TPR, int NV>
+int norm_launch(const BlockNormParams& p, cudaStream_t st) {
+  const long blocks = ceil_div(p.rows, 256 / TPR);
+  if (blocks > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  return launch(block_norm_kernel<T, VEC, TPR, NV>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p);
+}
+
+template <typename T>
+int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
+  if (vec) {
+    if (p.C <= 512) return norm_launch<T, 8, 32, 2>(p, st);
+    if (p.C <= 1280) return norm_launch<T, 8, 32, 5>(p, st);
+    if (p.C <= 2048) return norm_launch<T, 8, 32, 8>(p, st);
+    return norm_launch<T, 8, 256, 8>(p, st);
+  }
+  if (p.C <= 2048) return norm_launch<T, 1, 256, 8>(p, st);
+  return norm_launch<T, 1, 256, 64>(p, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
+  if (attn_args(a) != EDIT_OK) return 0;
+  // fewer rows can mean more parts: the most over all row counts up to rows_q.
+  // A row count only matters through its slots; take the largest of each.
+  AttnPlan pl;
+  attn_plan(a, a->rows_q, pl);
+  size_t most = pl.total;
+  const int R = pl.R;
+  for (int64_t rows = R - 1; rows < a->rows_q; rows += R) {
+    attn_plan(a, rows, pl);
+    if (pl.nsplit == 1) break;
+    if (pl.total > most) most = pl.total;
+  }
+  return most;
+}
+
+int edit_packed_attention_forward(const void* q, const void* k, const void* v, const edit_packed_attention* a,
+                                  void* out, void* stream) {
+  EDIT_TRY(attn_args(a));
+  if (!(a->scale > 0.f) || std::isinf(a->scale)) return EDIT_ERR_UNSUPPORTED;
+  if (!a->q_offsets || !a->k_offsets || !a->workspace) return EDIT_ERR_NULL;
+  if (a->rows_q > 0 && (!q || !out)) return EDIT_ERR_NULL;
+  if (a->rows_k > 0 && (!k || !v)) return EDIT_ERR_NULL;
+  const int64_t wq = static_cast<int64_t>(a->heads) * a->d, wk = static_cast<int64_t>(a->kv_heads) * a->d;
+  EDIT_TRY(check_ld(a->ldq, wq));
+  EDIT_TRY(check_ld(a->ldo, wq));
+  EDIT_TRY(check_ld(a->ldk, wk));
+  EDIT_TRY(check_ld(a->ldv, wk));
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(a->workspace, 256) ||
+      !aligned(a->q_offsets, 4) || !aligned(a->k_offsets, 4) || !aligned(a->k_lens, 4))
+    return EDIT_ERR_ALIGN;
+  AttnPlan pl;
+  attn_plan(a, a->rows_q, pl);
+  if (a->workspace_bytes < pl.total) return EDIT_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  PackedAttnParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.out = out;
+  p.q_offsets = a->q_offsets;
+  p.k_offsets = a->k_offsets;
+  p.k_lens = a->k_lens;
+  p.ldq = a->ldq;
+  p.ldk = a->ldk;
+  p.ldv = a->ldv;
+  p.ldo = a->ldo;
+  p.rows_q = static_cast<int>(a->rows_q);
+  p.rows_k = static_cast<int>(a->rows_k);
+  p.heads = a->heads;
+  p.kv_heads = a->kv_heads;
+  p.d = a->d;
+  p.nseq = a->nseq;
+  p.causal = a->causal;
+  p.max_k = a->max_k;
+  p.scale = a->scale;
+  p.slots = pl.slots;
+  p.nsplit = pl.nsplit;
+  p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
+  p.status = reinterpret_cast<int*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->dtype == EDIT_BF16 ? attn_run<__nv_bfloat16>(p, st) : attn_run<float>(p, st);
+}
+
+size_t edit_delta_rule_workspace_bytes(const edit_delta_rule* a) {
+  if (delta_args(a, false) != EDIT_OK) return 0;
+  return kStatusBytes;
+}
+
+int edit_delta_rule_forward(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                            const edit_delta_rule* a, const float* state_in, float* state_out, void* out,
+                            void* stream) {
+  EDIT_TRY(delta_args(a, false));
+  EDIT_TRY(delta_call(q, k, v, g, beta, a, a->rows, out));
+  if (!a->offsets || !a->workspace) return EDIT_ERR_NULL;
+  if (!aligned(a->workspace, 256) || !aligned(a->offsets, 4) || !aligned(state_in, 16) || !aligned(state_out, 16))
+    return EDIT_ERR_ALIGN;
+  if (a->workspace_bytes < kStatusBytes) return EDIT_ERR_WORKSPACE;
+  DeltaParams p = delta_params(q, k, v, g, beta, a, out);
+  p.offsets = a->offsets;
+  p.state_in = state_in;
+  p.state_out = state_out;
+  p.status = static_cast<int*>(a->workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16>(p, st) : delta_recurrent<float>(p, st);
+}
+
+int edit_delta_rule_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                         const edit_delta_rule* a, float* state, void* out, void* stream) {
+  EDIT_TRY(delta_args(a, true));
+  EDIT_TRY(delta_call(q, k, v, g, beta, a, a->nseq, out));
+  if (!state) return EDIT_ERR_NULL;
+  if (!aligned(state, 16)) return EDIT_ERR_ALIGN;
+  DeltaParams p = delta_params(q, k, v, g, beta, a, out);
+  p.rows = a->nseq;
+  p.state_in = state;
+  p.state_out = state;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16>(p, st) : delta_recurrent<float>(p, st);
+}
+
+int edit_block_norm_forward(const void* x, const void* y, const edit_block_norm* a, void* r, void* h, void* stream) {
+  if (!a) return EDIT_ERR_NULL;
+  if (a->dtype != EDIT_F32 && a->dtype != EDIT_BF16) return EDIT_ERR_DTYPE;
+  if (a->C < 1 || a->samples < 1 || a->rows < 0) return EDIT_ERR_SHAPE;
+  if (a->norm_post < EDIT_NORM_NONE || a->norm_post > EDIT_NORM_RMS || a->norm_pre < EDIT_NORM_NONE ||
+      a->norm_pre > EDIT_NORM_RMS || a->gate_act < EDIT_GATE_LINEAR || a->gate_act > EDIT_GATE_TANH)
+    return EDIT_ERR_UNSUPPORTED;
+  if ((a->norm_post == EDIT_NORM_NONE && (a->post_w || a->post_b)) ||
+      (a->norm_pre == EDIT_NORM_NONE && (a->pre_w || a->pre_b)))
+    return EDIT_ERR_UNSUPPORTED;
+  if (a->C > 16384 || a->rows > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (a->rows > 0 && (!x || (!r && !h))) return EDIT_ERR_NULL;
+  if (r && r == h) return EDIT_ERR_SHAPE;
+  const bool mods = a->gate || a->scale || a->shift;
+  if (a->ldx < a->C || (y && a->ldy < a->C) || (r && a->ldr < a->C) || (h && a->ldh < a->C) ||
+      (mods && a->samples > 1 && a->ld_mod < a->C))
+    return EDIT_ERR_SHAPE;
+  if (!a->offsets) {
+    if (a->rows_per_sample < 1 || ceil_div(a->rows, a->rows_per_sample) > a->samples) return EDIT_ERR_SHAPE;
+  } else if (!aligned(a->offsets, 4)) {
+    return EDIT_ERR_ALIGN;
+  }
+  // an output may be an input's buffer only row for row
+  if ((r && r == x && a->ldr != a->ldx) || (h && h == x && a->ldh != a->ldx) || (r && r == y && a->ldr != a->ldy) ||
+      (h && h == y && a->ldh != a->ldy))
+    return EDIT_ERR_SHAPE;
+  const uintptr_t es = a->dtype == EDIT_BF16 ? 2 : 4;
+  const void* ptrs[] = {x, y, r, h, a->post_w, a->post_b, a->pre_w, a->pre_b,
+                        a->gate0, a->scale0, a->shift0, a->gate, a->scale, a->shift};
+  bool vec = a->C % 8 == 0 && a->ldx % 8 == 0 && (!y || a->ldy % 8 == 0) && (!r || a->ldr % 8 == 0) &&
+             (!h || a->ldh % 8 == 0) && (!mods || a->samples == 1 || a->ld_mod % 8 == 0);
+  for (const void* t : ptrs) {
+    if (!aligned(t, es)) return EDIT_ERR_ALIGN;
+    vec = vec && aligned(t, 16);
+  }
+  if (a->rows == 0) return EDIT_OK;
+  BlockNormParams p = {};
+  p.x = x;
+  p.y = y;
+  p.r = r;
+  p.h = h;
+  p.post_w = a->post_w;
+  p.post_b = a->post_b;
+  p.pre_w = a->pre_w;
+  p.pre_b = a->pre_b;
+  p.gate0 = a->gate0;
+  p.scale0 = a->scale0;
+  p.shift0 = a->shift0;
+  p.gate = a->gate;
+  p.scale = a->scale;
+  p.shift = a->shift;
+  p.offsets = a->offsets;
+  p.rows = a->rows;
+  p.rows_per_sample = a->rows_per_sample;
+  p.ldx = a->ldx;
+  p.ldy = a->ldy;
+  p.ldr = a->ldr;
+  p.ldh = a->ldh;
+  p.ld_mod = a->samples > 1 ? a->ld_mod : 0;
+  p.C = a->C;
+  p.samples = a->samples;
+  p.post = a->norm_post;
+  p.pre = a->norm_pre;
+  p.act = a->gate_act;
+  p.eps = a->eps;
+  p.rho = a->res_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->dtype == EDIT_BF16 ? norm_run<__nv_bfloat16>(p, vec, st) : norm_run<float>(p, vec, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,218 @@
+"""The gated delta rule through the C ABI against the token-by-token 64-bit
+form, within the bounds of packed_ref.delta_rule."""
+import pytest
+import torch
+
+import packed_ref as R
+from linear_compressed_attention_b200 import binding as bd
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def offsets(lens):
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    return at
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def inputs(seed, dtype, rows, hq, h, dk, dv, rate=0.3, shared=0.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def n(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    q, k, v = n(rows, hq, dk), n(rows, hq, dk) + shared, n(rows, h, dv)
+    return (q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), -rate * n(rows, h).exp(), torch.sigmoid(2 * n(rows, h)))
+
+
+def check(out, state, ref, at):
+    o, s, ob, sb = ref
+    n = at[-1]
+    e = (out[:n].double() - o[:n]).norm(dim=-1)
+    assert torch.isfinite(out[:n]).all()
+    assert (e <= ob[:n]).all(), float((e / ob[:n]).max())
+    if state is not None:
+        e = (state.double() - s).flatten(2).norm(dim=-1)
+        assert (e <= sb).all(), float((e / sb).max())
+
+
+SHAPES = [(2, 4, 64, 64), (1, 2, 128, 128), (3, 3, 72, 72), (2, 2, 32, 96), (1, 3, 8, 256), (2, 2, 128, 40), (1, 1, 96, 64)]
+LENS = {"ragged": [1, 64, 0, 65, 130, 63], "long": [515], "two": [127, 129], "ones": [1] * 9}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", sorted(LENS))
+@pytest.mark.parametrize("hq,h,dk,dv", SHAPES)
+def test_matches_token_by_token(dtype, lens, hq, h, dk, dv):
+    at = offsets(LENS[lens])
+    rows = at[-1] + 3
+    q, k, v, g, beta = inputs(dk + dv, dtype, rows, hq, h, dk, dv)
+    S = len(at) - 1
+    state = torch.randn(S, h, dk, dv, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    op = bd.DeltaRule(hq, h, dk, dv, S, rows, dtype, scale=dk ** -0.5)
+    ref = R.delta_rule(q, k, v, g, beta, at, state, dk ** -0.5, True)
+    outs = []
+    for _ in range(2):
+        out, so = torch.full_like(v, 7.0), torch.full_like(state, 7.0)
+        op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=so, out=out)
+        assert op.status() == 0
+        check(out, so, ref, at)
+        assert (out[at[-1]:] == 7.0).all()
+        outs.append((out, so))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    # from zeros, dropping the state; and in place
+    out0 = op.forward(q, k, v, g, beta, ints(at), out=torch.full_like(v, 7.0))
+    check(out0, None, R.delta_rule(q, k, v, g, beta, at, None, dk ** -0.5, True), at)
+    same = state.clone()
+    out1 = op.forward(q, k, v, g, beta, ints(at), state_in=same, state_out=same, out=torch.full_like(v, 7.0))
+    assert torch.equal(out1, outs[0][0]) and torch.equal(same, outs[0][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,h,dk,dv", SHAPES)
+def test_step_is_one_token(dtype, hq, h, dk, dv):
+    S = 5
+    q, k, v, g, beta = inputs(7, dtype, S, hq, h, dk, dv)
+    state = torch.randn(S, h, dk, dv, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    op = bd.DeltaRule(hq, h, dk, dv, S, 0, dtype, scale=0.7)
+    ref = R.delta_rule(q, k, v, g, beta, list(range(S + 1)), state, 0.7, True)
+    mine = state.clone()
+    out = op.step(q, k, v, g, beta, mine)
+    check(out, mine, ref, [0, S])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_then_single_tokens_is_the_whole_sequence(dtype):
+    hq, h, dk, dv = 2, 4, 64, 64
+    lens = [100, 3]
+    q, k, v, g, beta = inputs(8, dtype, 2 * 120, hq, h, dk, dv)
+    at = [0, 120, 240]
+    ref = R.delta_rule(q, k, v, g, beta, at, None, 0.125, True)
+    op = bd.DeltaRule(hq, h, dk, dv, 2, 240, dtype)
+    rows = [torch.arange(at[s], at[s] + lens[s], device="cuda") for s in range(2)]
+    first = torch.cat(rows)
+    state = torch.zeros(2, h, dk, dv, device="cuda")
+    out = torch.zeros_like(v)
+    out[first] = op.forward(q[first], k[first], v[first], g[first], beta[first], ints(offsets(lens)), state_out=state)
+    for t in range(17):
+        r = torch.tensor([at[s] + lens[s] + t for s in range(2)], device="cuda")
+        out[r] = op.step(q[r], k[r], v[r], g[r], beta[r], state)
+    for s in range(2):
+        r = slice(at[s], at[s] + lens[s] + 17)
+        assert ((out[r].double() - ref[0][r]).norm(dim=-1) <= ref[2][r] * 1.01).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[200], [65, 1]])
+def test_without_the_norm_and_with_keys_alike(dtype, lens):
+    # keys that nearly repeat: the triangular system of a chunk is far from the identity
+    at = offsets(lens)
+    q, k, v, g, beta = inputs(9, dtype, at[-1], 1, 2, 64, 64, rate=0.01, shared=3.0)
+    op = bd.DeltaRule(1, 2, 64, 64, len(lens), at[-1], dtype)
+    so = torch.zeros(len(lens), 2, 64, 64, device="cuda")
+    out = op.forward(q, k, v, g, beta, ints(at), state_out=so)
+    check(out, so, R.delta_rule(q, k, v, g, beta, at, None, 0.125, True), at)
+    # unit keys given as they are
+    kn = (k.float() / k.float().norm(dim=-1, keepdim=True) * 0.98).to(DT[dtype])
+    qn = (q.float() / q.float().norm(dim=-1, keepdim=True)).to(DT[dtype])
+    op = bd.DeltaRule(1, 2, 64, 64, len(lens), at[-1], dtype, qk_norm=False)
+    out = op.forward(qn, kn, v, g, beta, ints(at), state_out=so)
+    check(out, so, R.delta_rule(qn, kn, v, g, beta, at, None, 0.125, False), at)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_forgetting_all_and_nothing(dtype):
+    at = [0, 150]
+    q, k, v, g, beta = inputs(10, dtype, 150, 1, 2, 64, 64)
+    g = g.clone()
+    g[40] = -float("inf")
+    g[41, 0] = -1e30
+    g[100:110] = 0.0
+    beta = beta.clone()
+    beta[20:30] = 0.0
+    beta[120] = 1.0
+    op = bd.DeltaRule(1, 2, 64, 64, 1, 150, dtype)
+    so = torch.zeros(1, 2, 64, 64, device="cuda")
+    out = op.forward(q, k, v, g, beta, ints(at), state_out=so)
+    check(out, so, R.delta_rule(q, k, v, g, beta, at, None, 0.125, True), at)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_zero_keys_and_queries(dtype):
+    at = [0, 70]
+    q, k, v, g, beta = inputs(11, dtype, 70, 1, 1, 64, 64)
+    q[5] = 0
+    k[7:9] = 0
+    op = bd.DeltaRule(1, 1, 64, 64, 1, 70, dtype)
+    out = op.forward(q, k, v, g, beta, ints(at))
+    assert (out[5] == 0).all()
+    check(out, None, R.delta_rule(q, k, v, g, beta, at, None, 0.125, True), at)
+
+
+def test_strided_inputs():
+    hq, h, d, n = 2, 4, 64, 140
+    q0, k0, v0, g0, b0 = inputs(12, "bf16", n, hq, h, d, d)
+    qkv = torch.cat([q0, k0, v0], 1)
+    gb = torch.cat([g0, b0], 1)
+    q, k, v = qkv[:, :hq], qkv[:, hq:2 * hq], qkv[:, 2 * hq:]
+    op = bd.DeltaRule(hq, h, d, d, 1, n, "bf16")
+    wide = torch.full((n, h + 2, d), 3.0, device="cuda", dtype=torch.bfloat16)
+    op.forward(q, k, v, gb[:, :h], gb[:, h:], ints([0, n]), out=wide[:, :h])
+    assert torch.equal(wide[:, :h], op.forward(q0, k0, v0, g0, b0, ints([0, n])))
+    assert (wide[:, h:] == 3.0).all()
+
+
+@pytest.mark.parametrize("at", [[0, 20, 10], [-3, 10, 20], [0, 10, 50], [2 ** 31 - 1, -2 ** 31, 7]])
+def test_bad_offsets_are_recorded_and_stay_inside(at):
+    for dtype in ("bf16", "f32"):
+        q, k, v, g, beta = inputs(13, dtype, 20, 1, 2, 64, 64)
+        guard = torch.full((24, 2, 64), 5.0, device="cuda", dtype=DT[dtype])
+        op = bd.DeltaRule(1, 2, 64, 64, 2, 20, dtype)
+        op.forward(q, k, v, g, beta, ints(at), out=guard[2:22])
+        assert op.status() == -2
+        assert (guard[:2] == 5.0).all() and (guard[22:] == 5.0).all()
+        op.forward(q, k, v, g, beta, ints([0, 10, 20]), out=guard[2:22])
+        assert op.status() == 0
+
+
+def test_no_rows_copies_the_states():
+    op = bd.DeltaRule(2, 4, 64, 64, 3, 0, "bf16")
+    e = torch.empty(0, 2, 64, device="cuda", dtype=torch.bfloat16)
+    ev = torch.empty(0, 4, 64, device="cuda", dtype=torch.bfloat16)
+    z = torch.empty(0, 4, device="cuda")
+    s = torch.randn(3, 4, 64, 64, device="cuda")
+    so = torch.zeros_like(s)
+    op.forward(e, e, ev, z, z, ints([0, 0, 0, 0]), state_in=s, state_out=so)
+    assert torch.equal(s, so)
+
+
+def test_captured_call_replays_with_other_lengths():
+    hq, h, d, n = 2, 4, 64, 300
+    q, k, v, g, beta = inputs(14, "bf16", n, hq, h, d, d)
+    at = ints([0, 100, n])
+    out, so = torch.zeros_like(v), torch.zeros(2, h, d, d, device="cuda")
+    op = bd.DeltaRule(hq, h, d, d, 2, n, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        op.forward(q, k, v, g, beta, at, state_out=so, out=out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            op.forward(q, k, v, g, beta, at, state_out=so, out=out)
+    torch.cuda.synchronize()
+    other = bd.DeltaRule(hq, h, d, d, 2, n, "bf16")
+    for now in ([0, 100, n], [0, 0, 77], [0, 299, n]):
+        at.copy_(ints(now))
+        out.fill_(2.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        s2 = torch.zeros_like(so)
+        eager = other.forward(q, k, v, g, beta, at, state_out=s2, out=torch.full_like(v, 2.0))
+        assert torch.equal(out, eager) and torch.equal(so, s2)
+        check(out, so, R.delta_rule(q, k, v, g, beta, now, None, 0.125, True), now)
