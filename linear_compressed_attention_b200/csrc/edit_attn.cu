@@ -1928,6 +1928,10 @@ int common_checks(const void* x, const void* out, const edit_attn_weights* w, vo
 namespace edit {
 void count_launch() { ++g_launches; }
 int device_sms() { return num_sms(); }
+bool bf16_tensor_map(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
+                     const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+  return encode(m, rank, base, dims, strides_bytes, box);
+}
 }  // namespace edit
 
 // =================================================================== C ABI

@@ -14,6 +14,7 @@
 #include "delta_rule.cuh"
 #include "host.h"
 #include "packed_attn.cuh"
+#include "packed_attn_tc.cuh"
 
 using namespace edit;
 
@@ -61,12 +62,19 @@ int check_ld(int64_t ld, int64_t width) {
 constexpr size_t kStatusBytes = 256;
 
 struct AttnPlan {
-  int R;  // tokens of a row tile
   int slots, nsplit;
   size_t part_o, part_ml, total;
 };
 
-int attn_rows(int dtype, int G) { return 64 / G; }
+// bf16 calls whose sequences have at most 128 packed rows on average take one
+// row tile a block and two blocks an SM, others two row tiles a block.
+int attn_row_tiles(const edit_packed_attention* a, int64_t rows) {
+  return rows * (a->heads / a->kv_heads) <= 128 * static_cast<int64_t>(a->nseq) ? 1 : 2;
+}
+int attn_rows(const edit_packed_attention* a, int64_t rows) {
+  const int G = a->heads / a->kv_heads;
+  return a->dtype == EDIT_BF16 ? attn_row_tiles(a, rows) * (128 / G) : 64 / G;
+}
 
 int attn_args(const edit_packed_attention* a) {
   if (!a) return EDIT_ERR_NULL;
@@ -76,7 +84,7 @@ int attn_args(const edit_packed_attention* a) {
     return EDIT_ERR_SHAPE;
   if (a->d % 8 != 0 || a->d > 128 || a->heads / a->kv_heads > 64 || a->kv_heads > 65535) return EDIT_ERR_UNSUPPORTED;
   if (a->rows_q > INT32_MAX || a->rows_k > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
-  if (a->rows_q / attn_rows(a->dtype, a->heads / a->kv_heads) + a->nseq > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (a->rows_q + a->nseq > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
   return EDIT_OK;
 }
 
@@ -88,9 +96,9 @@ int attn_nsplit(long slots, const edit_packed_attention* a, int sms) {
   return static_cast<int>(n < 1 ? 1 : n);
 }
 
-void attn_plan(const edit_packed_attention* a, int64_t rows, AttnPlan& pl) {
-  pl.R = attn_rows(a->dtype, a->heads / a->kv_heads);
-  pl.slots = static_cast<int>(rows / pl.R + a->nseq);
+// The plan of `rows` query rows in tiles of R.
+void attn_plan(const edit_packed_attention* a, int64_t rows, int R, AttnPlan& pl) {
+  pl.slots = static_cast<int>(rows / R + a->nseq);
   pl.nsplit = rows > 0 ? attn_nsplit(pl.slots, a, device_sms()) : 1;
   const size_t items = static_cast<size_t>(pl.nsplit) * rows * a->heads;
   pl.part_o = kStatusBytes;
@@ -104,9 +112,47 @@ int attn_simt(const PackedAttnParams& p, cudaStream_t st) {
   return launch(packed_attn_simt_kernel<T, DP>, dim3(p.slots, p.kv_heads, p.nsplit), dim3(256), smem, st, p);
 }
 
+template <int DP, int NQ>
+int attn_tc(const PackedAttnParams& p, cudaStream_t st) {
+  using Cfg = AttnTcCfg<DP, NQ>;
+  const int G = p.heads / p.kv_heads;
+  const cuuint64_t d = p.d, gl = G, kl = p.kv_heads;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[4] = {d, gl, kl, static_cast<cuuint64_t>(p.rows_q)};
+    const cuuint64_t strides[3] = {d * 2, gl * d * 2, static_cast<cuuint64_t>(p.ldq) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(128 / G)};
+    if (!bf16_tensor_map(&mq, 4, p.q, dims, strides, box)) return EDIT_ERR_CUDA;
+  }
+  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint64_t dims[3] = {d, kl, static_cast<cuuint64_t>(p.rows_k)};
+  const cuuint64_t sk[2] = {d * 2, static_cast<cuuint64_t>(p.ldk) * 2}, sv[2] = {d * 2, static_cast<cuuint64_t>(p.ldv) * 2};
+  if (!bf16_tensor_map(&mk, 3, p.k, dims, sk, box) || !bf16_tensor_map(&mv, 3, p.v, dims, sv, box))
+    return EDIT_ERR_CUDA;
+  return launch(packed_attn_tc_kernel<DP, NQ>, dim3(p.slots, p.kv_heads, p.nsplit), dim3(Cfg::THREADS), Cfg::SMEM, st,
+                mq, mk, mv, p);
+}
+
+template <int NQ>
+int attn_tc_width(const PackedAttnParams& p, cudaStream_t st) {
+  if (p.d <= 64) return attn_tc<64, NQ>(p, st);
+  if (p.d <= 80) return attn_tc<80, NQ>(p, st);
+  return attn_tc<128, NQ>(p, st);
+}
+
 template <typename T>
-int attn_run(const PackedAttnParams& p, cudaStream_t st) {
-  EDIT_TRY(p.d <= 64 ? (attn_simt<T, 64>(p, st)) : (attn_simt<T, 128>(p, st)));
+int attn_run(PackedAttnParams p, int row_tiles, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2) {
+    if (p.rows_q == 0 || p.rows_k == 0) {  // no tensor to describe: the offsets are checked, rows get zeros
+      p.slots = p.rows_q / (64 / (p.heads / p.kv_heads)) + p.nseq;
+      p.nsplit = 1;
+      EDIT_TRY((attn_simt<T, 128>(p, st)));
+    } else {
+      EDIT_TRY(row_tiles == 1 ? attn_tc_width<1>(p, st) : attn_tc_width<2>(p, st));
+    }
+  } else {
+    EDIT_TRY(p.d <= 64 ? (attn_simt<T, 64>(p, st)) : (attn_simt<T, 128>(p, st)));
+  }
   if (p.nsplit == 1) return EDIT_OK;
   return launch(packed_attn_join_kernel<T>, dim3(static_cast<unsigned>(ceil_div(static_cast<long>(p.rows_q) * p.heads, 4))),
                 dim3(128), 0, st, p);
@@ -203,16 +249,19 @@ extern "C" {
 
 size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
   if (attn_args(a) != EDIT_OK) return 0;
-  // fewer rows can mean more parts: the most over all row counts up to rows_q.
-  // A row count only matters through its slots; take the largest of each.
-  AttnPlan pl;
-  attn_plan(a, a->rows_q, pl);
-  size_t most = pl.total;
-  const int R = pl.R;
-  for (int64_t rows = R - 1; rows < a->rows_q; rows += R) {
-    attn_plan(a, rows, pl);
-    if (pl.nsplit == 1) break;
-    if (pl.total > most) most = pl.total;
+  // Fewer rows can mean more parts: the most over all row counts up to rows_q and
+  // both tile heights. Rows with the same number of slots have the same parts, so
+  // the last of each are enough.
+  size_t most = kStatusBytes;
+  const int G = a->heads / a->kv_heads;
+  const int heights[2] = {a->dtype == EDIT_BF16 ? 128 / G : 64 / G, a->dtype == EDIT_BF16 ? 2 * (128 / G) : 64 / G};
+  for (int R : heights) {
+    for (int64_t rows = R - 1;; rows += R) {
+      AttnPlan pl;
+      attn_plan(a, rows < a->rows_q ? rows : a->rows_q, R, pl);
+      if (pl.total > most) most = pl.total;
+      if (pl.nsplit == 1 || rows >= a->rows_q) break;
+    }
   }
   return most;
 }
@@ -233,7 +282,7 @@ int edit_packed_attention_forward(const void* q, const void* k, const void* v, c
       !aligned(a->q_offsets, 4) || !aligned(a->k_offsets, 4) || !aligned(a->k_lens, 4))
     return EDIT_ERR_ALIGN;
   AttnPlan pl;
-  attn_plan(a, a->rows_q, pl);
+  attn_plan(a, a->rows_q, attn_rows(a, a->rows_q), pl);
   if (a->workspace_bytes < pl.total) return EDIT_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   PackedAttnParams p = {};
@@ -263,7 +312,7 @@ int edit_packed_attention_forward(const void* q, const void* k, const void* v, c
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
   p.status = reinterpret_cast<int*>(ws);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a->dtype == EDIT_BF16 ? attn_run<__nv_bfloat16>(p, st) : attn_run<float>(p, st);
+  return a->dtype == EDIT_BF16 ? attn_run<__nv_bfloat16>(p, attn_row_tiles(a, a->rows_q), st) : attn_run<float>(p, 0, st);
 }
 
 size_t edit_delta_rule_workspace_bytes(const edit_delta_rule* a) {
