@@ -37,14 +37,24 @@ struct AttnTcCfg {
   static constexpr int SLOTS = NQ == 1 ? (DP == 64 ? 4 : 2) : (DP == 64 ? 8 : 5);  // ring of K and V tiles
   static constexpr int V_PERIOD = SLOTS % 2 ? SLOTS : SLOTS / 2;  // key tiles between two uses of a slot for V
   static constexpr int BARS = NQ * 4 + 4 * SLOTS;
-  static constexpr int SMEM = 1024 + (NQ + SLOTS) * TILE + BARS * 8 + 32;
+  static constexpr int SMEM = 1024 + (NQ + SLOTS) * TILE + BARS * 8 + 16 + 96;
   static_assert(SMEM * (NQ == 1 ? 2 : 1) + (NQ == 1 ? 2048 : 0) <= 232448 + 1024, "shared memory");
-  // two row tiles: launched with 168 registers a thread, 208 for the softmax warps and 88 for the others (256 x 208 +
-  // 128 x 88 = 384 x 168)
+  // two row tiles: launched with 168 registers a thread, 200 for the softmax warps and 104 for the others (256 x 200 +
+  // 128 x 104 = 384 x 168)
   static constexpr int THREADS = NQ * 128 + 128;
   static constexpr int TMEM = NQ * 256;             // S of tile i at 128 i, O behind them
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128);
   static constexpr uint32_t IDESC_O = idesc_bf16_f32(128, DP) | IDESC_B_MN;
+};
+
+template <int NQ>
+struct AttnBlock {
+  bool some;        // the slot has rows
+  AttnItem it;
+  int tiles[NQ];    // key tiles of each row tile
+  int most;         // the most of them
+  int all_see;      // keys that every row sees: 0 .. all_see - 1; V tiles reaching beyond have masked keys
+  int clean;        // key tiles before the first of those
 };
 
 template <int R>
@@ -72,9 +82,7 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 __device__ __forceinline__ bool attn_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = attn_wait(bar, parity, abort_flag, status) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  return __all_sync(0xffffffffu, attn_wait(bar, parity, abort_flag, status));  // (every lane polls)
 }
 
 template <int DP, int NQ>
@@ -97,29 +105,35 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_load + SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* odd_values = abort_flag + 1;  // the guard cleared values that are not finite
+  AttnBlock<NQ>* work = reinterpret_cast<AttnBlock<NQ>*>(tmem_slot + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int W_TMA = NQ * 4, W_MMA = W_TMA + 1, W_GUARD = W_TMA + 2;
   pdl_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
     check_offsets(p.q_offsets, p.rows_q, p.k_offsets, p.rows_k, p.k_lens, p.max_k, p.nseq, p.status);
-  const int G = p.heads / p.kv_heads, R = 128 / G, hk = blockIdx.y;  // R tokens a row tile
-  AttnItem it;
-  if (!attn_item<128>(p, p.slots - 1 - blockIdx.x, blockIdx.z, NQ * R, it)) return;
-  // key tiles of each row tile: those its last row sees (within this split)
-  int tiles[NQ], most = 0;
+  // the block's work, found by one warp; every warp takes what it needs from shared memory after the roles part
+  // (held in registers across them, it costs the softmax warps theirs)
+  if (warp == 0) {
+    const int G = p.heads / p.kv_heads, R = 128 / G;  // R tokens a row tile
+    AttnBlock<NQ> w;
+    w.some = attn_item<128>(p, p.slots - 1 - blockIdx.x, blockIdx.z, NQ * R, w.it);
+    w.most = 0;
+    if (w.some) {
+      // key tiles of each row tile: those its last row sees (within this split)
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int n = min(it.ntok - i * R, R);  // tokens
-    int kend = it.kend;
-    if (p.causal) kend = min(kend, it.tok0 + i * R + n + it.lk - it.lq);
-    tiles[i] = n > 0 && kend > it.kbeg ? (kend - it.kbeg + 127) / 128 : 0;
-    most = max(most, tiles[i]);
+      for (int i = 0; i < NQ; ++i) {
+        const int n = min(w.it.ntok - i * R, R);  // tokens
+        int kend = w.it.kend;
+        if (p.causal) kend = min(kend, w.it.tok0 + i * R + n + w.it.lk - w.it.lq);
+        w.tiles[i] = n > 0 && kend > w.it.kbeg ? (kend - w.it.kbeg + 127) / 128 : 0;
+        w.most = max(w.most, w.tiles[i]);
+      }
+      w.all_see = min(w.it.kend, p.causal ? clamp_int(w.it.tok0 + 1 + w.it.lk - w.it.lq, 0, w.it.lk) : w.it.lk);
+      w.clean = max(0, min(w.most, (w.all_see - w.it.kbeg) / 128));
+    }
+    if (lane == 0) *work = w;
   }
-  // keys that every row sees: 0 .. all_see - 1; V tiles reaching beyond have masked keys
-  const int all_see = min(it.kend, p.causal ? clamp_int(it.tok0 + 1 + it.lk - it.lq, 0, it.lk) : it.lk);
-  const int clean = max(0, min(most, (all_see - it.kbeg) / 128));  // tiles before the first with masked keys
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
       mbar_init(&q_full[i], 1);
@@ -137,19 +151,24 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     *odd_values = 0;
     fence_mbar_init();
   }
+  __syncthreads();
+  if (!work->some) return;
   if (warp == W_MMA) tmem_alloc(tmem_slot, Cfg::TMEM);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp >= W_TMA) {
+    if constexpr (NQ == 2) regs_dec<104>();
     if (warp == W_TMA && lane == 0) {
       // ---------------------------------------------------------- producer: Q, then K_0 V_0 K_1 V_1 ...
+      const AttnItem it = work->it;
+      const int most = work->most, clean = work->clean, hk = blockIdx.y;
+      const int G = p.heads / p.kv_heads, R = 128 / G;
       bool ok = true;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        if (tiles[i] == 0) continue;
+        if (work->tiles[i] == 0) continue;
         mbar_arrive_expect_tx(&q_full[i], NBX * R * G * 128);
 #pragma unroll
         for (int b = 0; b < NBX; ++b)
@@ -175,21 +194,28 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
       }
     } else if (warp == W_MMA && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
+      const uint32_t tmem = *tmem_slot;
+      const int most = work->most, clean = work->clean;
+      int tiles[NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) tiles[i] = work->tiles[i];
       auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_wait(bar, parity, abort_flag, p.status); };
       auto scores = [&](int i, int t) {  // S_i = Q_i K_t^T
-        const uint32_t qa = smem_u32(sQ + i * TILE), ka = smem_u32(sKV + ((2 * t) % SLOTS) * TILE);
+        const uint64_t qd = sdesc_kmajor_sw128(smem_u32(sQ + i * TILE));
+        const uint64_t kd = sdesc_kmajor_sw128(smem_u32(sKV + ((2 * t) % SLOTS) * TILE));
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k)
-          umma_bf16(tmem + 128 * i, sdesc_kmajor_sw128(qa + (k >> 2) * BOX + (k & 3) * 32),
-                    sdesc_kmajor_sw128(ka + (k >> 2) * BOX + (k & 3) * 32), Cfg::IDESC_S, k > 0 ? 1u : 0u);
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint64_t step = ((k >> 2) * BOX + (k & 3) * 32) >> 4;
+          umma_bf16(tmem + 128 * i, qd + step, kd + step, Cfg::IDESC_S, k > 0 ? 1u : 0u);
+        }
         umma_commit(&s_full[i]);
       };
       auto weigh = [&](int i, int t) {  // O_i += P_i V_t
-        const uint32_t va = smem_u32(sKV + ((2 * t + 1) % SLOTS) * TILE);
+        const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(sKV + ((2 * t + 1) % SLOTS) * TILE), BOX);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          umma_bf16_ts(tmem + NQ * 128 + DP * i, tmem + 128 * i + 8 * k, sdesc_mnmajor_sw128(va + 2048 * k, BOX),
-                       Cfg::IDESC_O, (t > 0 || k > 0) ? 1u : 0u);
+          umma_bf16_ts(tmem + NQ * 128 + DP * i, tmem + 128 * i + 8 * k, vd + (2048 >> 4) * k, Cfg::IDESC_O,
+                       (t > 0 || k > 0) ? 1u : 0u);
         umma_commit(&o_full[i]);
       };
       bool ok = true;
@@ -229,15 +255,18 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
       }
     } else if (warp == W_GUARD) {
       // ---------------------------------------------------------- V guard
+      const int most = work->most, clean = work->clean, all_see = work->all_see;
+      const int kbeg = work->it.kbeg, kend = work->it.kend;
       for (int t = clean; t < most; ++t) {
-        const int s = (2 * t + 1) % SLOTS, key0 = it.kbeg + t * 128;
+        const int s = (2 * t + 1) % SLOTS, key0 = kbeg + t * 128;
         // (the load's issue first: before it, kv_full's parity could be that of a use two back)
         if (!attn_warp_wait(&v_load[s], ((t - clean) / Cfg::V_PERIOD) & 1, abort_flag, p.status) ||
             !attn_warp_wait(&kv_full[s], ((2 * t + 1) / SLOTS) & 1, abort_flag, p.status))
           break;
         uint8_t* v = sKV + s * TILE;
-        const int nk = min(128, it.kend - key0);          // rows behind are cleared
+        const int nk = min(128, kend - key0);             // rows behind are cleared
         const int from = clamp_int(all_see - key0, 0, nk);  // rows before are seen by all
+#pragma unroll 1
         for (int e = lane; e < NBX * (128 - from) * 8; e += 32) {
           const int b = e / ((128 - from) * 8), x = e % ((128 - from) * 8), r = from + (x >> 3);
           uint4* c = reinterpret_cast<uint4*>(v + b * BOX + r * 128 + (x & 7) * 16);
@@ -271,18 +300,21 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     }
     __syncwarp();
   } else {
-    constexpr bool HOLD = false;
+    constexpr bool HOLD = NQ == 2;
+    if constexpr (NQ == 2) regs_inc<200>();
     // ------------------------------------------------------------ softmax, output
     const int i = NQ == 2 ? warp >> 2 : 0;
     const int q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t tmem = *tmem_slot;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     const uint32_t tS = t_lane + 128 * i, tO = t_lane + NQ * 128 + DP * i;
-    const int T = NQ == 2 ? (i == 0 ? tiles[0] : tiles[NQ - 1]) : tiles[0];
-    const int tok = it.tok0 + i * R + r / G;  // of the sequence
-    const bool real = r < R * G && tok < it.lq;
+    const int T = work->tiles[i], kbeg = work->it.kbeg;
+    const int G = p.heads / p.kv_heads, R = 128 / G;
+    const int tok = work->it.tok0 + i * R + r / G;  // of the sequence
+    const bool real = r < R * G && tok < work->it.lq;
     const bool any = __any_sync(0xffffffffu, real);  // a warp without rows only keeps the barriers going
-    int see = it.kend;
-    if (p.causal) see = min(see, tok + 1 + it.lk - it.lq);
+    int see = work->it.kend;
+    if (p.causal) see = min(see, tok + 1 + work->it.lk - work->it.lq);
     const float c = p.scale * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f;  // maximum (of c S) that O and l refer to
     bool ok = true;
@@ -296,7 +328,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
         // S of the row, 64 keys at a time: held in registers with two row tiles, read
         // twice with one (which leaves registers for a second block on the SM)
         float s[HOLD ? 2 : 1][64];
-        const int n = see - (it.kbeg + t * 128);  // visible keys of this tile
+        const int n = see - (kbeg + t * 128);  // visible keys of this tile
         const bool masked = __any_sync(0xffffffffu, n < 128);
         auto fetch = [&](int half) {
           float(&v)[64] = s[HOLD ? half : 0];
@@ -367,8 +399,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     if (ok && T > 0) ok = attn_warp_wait(&o_full[i], (T - 1) & 1, abort_flag, p.status);
     if (ok && any) {
       tc_fence_after();
-      const long row = it.q0 + static_cast<long>(tok);
-      const int h = hk * G + r % G;
+      const long row = work->it.q0 + static_cast<long>(tok);
+      const int hk = blockIdx.y, h = hk * G + r % G;
       const long at = (blockIdx.z * static_cast<long>(p.rows_q) + row) * p.heads + h;
       const float inv = p.nsplit > 1 ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
       const bool odd = *odd_values;
@@ -383,10 +415,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
           for (int k = 0; k < 16; ++k) o[k] = 0.f;
         }
         if (odd && real) {  // values the guard cleared, for the rows that see them
-          for (int j = it.kbeg + clean * 128; j < see; ++j) {
+          for (int j = max(work->all_see, kbeg + work->clean * 128); j < see; ++j) {
             const __nv_bfloat16* vj = static_cast<const __nv_bfloat16*>(p.v) +
-                                      (it.k0 + static_cast<long>(j)) * p.ldv + hk * p.d + x;
-            if (j < all_see) continue;
+                                      (work->it.k0 + static_cast<long>(j)) * p.ldv + hk * p.d + x;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               if (x + k >= p.d) continue;
@@ -422,7 +453,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
   __syncthreads();
   if (warp == W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, Cfg::TMEM);
+    tmem_dealloc(*tmem_slot, Cfg::TMEM);
   }
 }
 
