@@ -512,7 +512,7 @@ EDIT_API int edit_packed_attention_forward(const void *q, const void *k, const v
  * two may be the same buffer (not overlap in another way). A sequence of no rows
  * copies its state.
  * d_k a multiple of 8 up to 128, d_v a multiple of 8 up to 256, ldq .. ldo
- * multiples of 8; else EDIT_ERR_UNSUPPORTED.
+ * multiples of 8, nseq at most 65535; else EDIT_ERR_UNSUPPORTED.
  * edit_delta_rule_step is one token for each of nseq sequences (row s belongs
  * to sequence s; offsets and rows are not read, no workspace): `state` is
  * updated in place. */

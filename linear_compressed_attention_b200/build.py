@@ -11,7 +11,7 @@ SRCS = [os.path.join(PKG, "csrc", f) for f in ("edit_attn.cu", "edit_noalloc.cu"
 OUT = os.path.join(PKG, "libedit_attn.so")
 DEPS = [os.path.join(PKG, "csrc", f) for f in ("edit_attn.cu", "edit_noalloc.cu", "common.cuh", "tc_gemm.cuh",
                                                 "tc_conv.cuh", "simt_kernels.cuh", "sdpa_tc.cuh", "packed_ops.cu",
-                                                "host.h", "packed_seq.cuh", "packed_attn.cuh", "packed_attn_tc.cuh", "delta_rule.cuh",
+                                                "host.h", "packed_seq.cuh", "packed_attn.cuh", "packed_attn_tc.cuh", "delta_rule.cuh", "delta_chunk.cuh",
                                                 "block_norm.cuh")]
 DEPS.append(os.path.join(ROOT, "include", "edit_attn.h"))
 

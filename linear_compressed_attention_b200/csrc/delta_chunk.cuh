@@ -1,0 +1,665 @@
+// The gated delta rule over whole prompts (bf16 calls of
+// edit_delta_rule_forward): chunks of 64 tokens on the tensor cores.
+//
+// With G the running sum of g within a chunk, k^ = rk k (rk the inverse norm, or
+// 1), S0 the state before the chunk and Gamma_ij = exp(G_i - G_j):
+//   T  = (I + strictly-lower(diag(beta) K^ K^^T . Gamma))^-1 diag(beta)
+//   U  = T (V - diag(e^G) K^ S0)
+//   O  = scale (diag(e^G) Q^ S0 + lower(Q^ K^^T . Gamma) U)
+//   S1 = e^G_64 S0 + (diag(e^(G_64 - G)) K^)^T U
+// T and P = lower(..) depend on no state: delta_prep_kernel forms them for all
+// chunks at once. delta_chunk_kernel then walks the chunks of one (sequence,
+// head); its columns of V, U, S and O are independent of each other, so a warp
+// owns 16 of them and keeps the transposed products in registers: the
+// accumulator layout of S^T, X^T = V^T - .., U^T is the operand layout of the
+// next product (mma.sync m16n8k16), and the whole chain of a chunk needs no
+// shared memory between its products and no block-wide wait. (The chain is three
+// dependent products of 16 x 64 x 128 and less for each warp: too small and too
+// serial for tcgen05's 128-row tiles to pay.)
+//
+// Precision: the state is fp32, and what flows into it keeps fp32's precision
+// on fp16 operands: an fp32 operand row is scaled by a power of two to below 2
+// and split into two fp16 halves (22 bits), k (8 bits) is exact in fp16 after
+// such a scaling, and T is split as well; the dropped product of two low halves
+// is 2^-22. (Two bf16 halves would leave 2^-17 and three would cost half as many
+// products again.) O is rounded to bf16, so its products take one half: fp16 for
+// Q^ S0, bf16 for P U, whose terms a decay may set many powers of two apart.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "delta_rule.cuh"
+
+namespace edit {
+
+constexpr int kDeltaL = 64;    // tokens a chunk
+constexpr int kDeltaLd = 72;   // row stride (fp16) of T and P: 16-byte rows without bank conflicts
+
+// Per (chunk slot, head): T high, T low [64][72] fp16, the scalars, P [64][72] bf16.
+enum { DS_FX, DS_T, DS_W, DS_FO, DS_A, DS_COUNT };  // rows of 64 fp32 scalars
+constexpr int kDeltaMat = kDeltaL * kDeltaLd * 2;
+constexpr int kDeltaScal = DS_COUNT * kDeltaL * 4;
+constexpr int kDeltaBlob = 3 * kDeltaMat + kDeltaScal;
+// Per (chunk slot, qk head): K, Q [64][DK + 8] fp16, each row scaled to below 2.
+__host__ __device__ constexpr int delta_kq_bytes(int DK) { return 2 * kDeltaL * (DK + 8) * 2; }
+
+struct DeltaChunkParams {
+  DeltaParams d;
+  uint8_t* blobs;     // [slots][heads] kDeltaBlob
+  uint8_t* kq;        // [slots][qk_heads] delta_kq_bytes
+  int slots;
+  int nseg;           // parts of a sequence's chunks (1: none)
+  float* trans;       // [nseq][heads][nseg - 1][d_k][d_v + d_k]: a part's [added state | transition]
+  float* starts;      // [nseq][heads][nseg - 1][d_k][d_v]: the state before parts 1 ..
+};
+
+// Power of two that brings |m| below 2 (down), and its inverse.
+__device__ __forceinline__ void pow2_scale(float m, float& down, float& up) {
+  int e = static_cast<int>((__float_as_uint(m) >> 23) & 0xff);
+  e = e < 1 ? 1 : (e > 253 ? 253 : e);
+  down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// x (a pair) as the fp16 pair nearest to it and the fp16 pair nearest to what is left.
+__device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_f16x2(x0 - f.x, x1 - f.y);
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- chunks by themselves
+// One block a (chunk, head). Warp w forms rows 16 w .. 16 w + 15 of K K^T and
+// Q K^T (exact bf16 products, fp32 sums); thread j < 64 then solves column j of
+// the unit triangular system by forward substitution in registers.
+template <int DK>
+struct DeltaPrepCfg {
+  static constexpr int LD = DK + 8;
+  static constexpr int SMEM = 2 * kDeltaL * LD * 2 + kDeltaL * 68 * 4 + kDeltaL * 65 * 4 + kDeltaL * 8 + 8 * kDeltaL * 4;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams p) {
+  pdl_wait();
+  const DeltaParams& d = p.d;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    check_offsets(d.offsets, d.rows, nullptr, 0, nullptr, 0, d.nseq, d.status);
+  constexpr int L = kDeltaL, LD = DeltaPrepCfg<DK>::LD;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  uint8_t* sm = dsm;
+  __nv_bfloat16* sK = reinterpret_cast<__nv_bfloat16*>(sm);
+  __nv_bfloat16* sQ = sK + L * LD;
+  float* sA = reinterpret_cast<float*>(sQ + L * LD);  // [64][68]
+  float* sT = sA + L * 68;                            // [64][65]
+  double* sG = reinterpret_cast<double*>(sT + L * 65);
+  float* sRk = reinterpret_cast<float*>(sG + L);
+  float *sRq = sRk + L, *sKd = sRq + L, *sKu = sKd + L, *sQd = sKu + L, *sQu = sQd + L, *sB = sQu + L;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slot = blockIdx.x, h = blockIdx.y, hq = h / (d.heads / d.qk_heads);
+  const int seq = seq_of_slot(d.offsets, d.nseq, static_cast<int>(d.rows), L, slot);
+  const SeqRows sr = seq_rows(d.offsets, seq, static_cast<int>(d.rows));
+  const int c = slot - (sr.begin / L + seq);
+  if (c < 0 || c * static_cast<long>(L) >= sr.len) return;
+  const int n = min(L, sr.len - c * L);
+  const long row0 = sr.begin + static_cast<long>(c) * L;
+
+  for (int e = tid; e < L * (DK / 8); e += 128) {
+    const int r = e / (DK / 8), x = (e % (DK / 8)) * 8;
+    uint4 k = make_uint4(0u, 0u, 0u, 0u), q = k;
+    if (r < n && x < d.d_k) {
+      k = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.k) + (row0 + r) * d.ldk + hq * d.d_k + x);
+      q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.q) + (row0 + r) * d.ldq + hq * d.d_k + x);
+    }
+    *reinterpret_cast<uint4*>(sK + r * LD + x) = k;
+    *reinterpret_cast<uint4*>(sQ + r * LD + x) = q;
+  }
+  if (tid < L) {  // running sums of g in fp64: differences of far sums keep their fp32 precision
+    double G = tid < n ? static_cast<double>(log_decay(d.g[(row0 + tid) * d.ldg + h])) : 0.0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double a = __shfl_up_sync(0xffffffffu, G, o);
+      if (lane >= o) G += a;
+    }
+    sG[tid] = G;
+    sB[tid] = tid < n ? d.beta[(row0 + tid) * d.ldb + h] : 0.f;
+  }
+  __syncthreads();
+  {
+    const int t = tid & 63;
+    const __nv_bfloat16* x = (tid < 64 ? sK : sQ) + t * LD;
+    float s = 0.f, m = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < DK; i += 8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(x + i);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
+        s = fmaf(a, a, fmaf(b, b, s));
+        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+      }
+    }
+    float down, up;
+    pow2_scale(m, down, up);
+    const float r = t >= n ? 0.f : (d.qk_norm ? 1.f / sqrtf(s + d.qk_eps) : 1.f);
+    (tid < 64 ? sRk : sRq)[t] = r;
+    (tid < 64 ? sKd : sQd)[t] = down;
+    (tid < 64 ? sKu : sQu)[t] = up;
+    if (tid >= 32 && tid < 64) sG[tid] += sG[31];
+  }
+  __syncthreads();
+  uint8_t* blob = p.blobs + (static_cast<long>(slot) * d.heads + h) * kDeltaBlob;
+  float* scal = reinterpret_cast<float*>(blob + 2 * kDeltaMat);
+  {
+    // K K^T and Q K^T of this warp's 16 rows, columns up to its diagonal block
+    float kk[8][4] = {}, qk[8][4] = {};
+    const uint32_t ka = smem_u32(sK), qa = smem_u32(sQ);
+    const uint32_t arow = (16 * warp + (lane & 15)) * LD * 2 + (lane >> 4) * 16;
+    const uint32_t brow = ((lane & 7) + ((lane >> 4) << 3)) * LD * 2 + ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int k = 0; k < DK / 16; ++k) {
+      uint32_t a[4], q[4];
+      ldsm_x4(ka + arow + 32 * k, a);
+      ldsm_x4(qa + arow + 32 * k, q);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t > warp) break;
+        uint32_t b[4];
+        ldsm_x4(ka + brow + t * 16 * LD * 2 + 32 * k, b);
+        mma_bf16(kk[2 * t], a, b[0], b[1]);
+        mma_bf16(kk[2 * t + 1], a, b[2], b[3]);
+        mma_bf16(qk[2 * t], q, b[0], b[1]);
+        mma_bf16(qk[2 * t + 1], q, b[2], b[3]);
+      }
+    }
+    __nv_bfloat16* P = reinterpret_cast<__nv_bfloat16*>(blob + 2 * kDeltaMat + kDeltaScal);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      if (t > 2 * warp + 1) break;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int i = 16 * warp + (lane >> 2) + 8 * r, j0 = 8 * t + 2 * (lane & 3);
+        float pv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = j0 + e;
+          const float gam = j <= i ? expf(static_cast<float>(sG[i] - sG[j])) * sRk[j] : 0.f;
+          sA[i * 68 + j] = j < i ? sB[i] * sRk[i] * gam * kk[t][2 * r + e] : 0.f;
+          pv[e] = j <= i ? d.scale * gam * sRq[i] * qk[t][2 * r + e] : 0.f;
+        }
+        *reinterpret_cast<uint32_t*>(P + i * kDeltaLd + j0) = pack_bf16x2(pv[0], pv[1]);
+      }
+    }
+  }
+  if (tid < L) {
+    const float eG = expf(static_cast<float>(sG[tid])), rest = expf(static_cast<float>(sG[L - 1] - sG[tid]));
+    scal[DS_FX * L + tid] = eG * sRk[tid] * sKu[tid];
+    scal[DS_W * L + tid] = rest * sRk[tid] * sKu[tid];
+    scal[DS_FO * L + tid] = d.scale * eG * sRq[tid] * sQu[tid];
+    scal[DS_A * L + tid] = expf(static_cast<float>(sG[L - 1]));
+  }
+  if (h % (d.heads / d.qk_heads) == 0) {  // fp16 K and Q for all heads that share them
+    __half* K16 = reinterpret_cast<__half*>(p.kq + (static_cast<long>(slot) * d.qk_heads + hq) * delta_kq_bytes(DK));
+    for (int e = tid; e < 2 * L * (DK / 8); e += 128) {
+      const int which = e / (L * (DK / 8)), f = e % (L * (DK / 8)), r = f / (DK / 8), x = (f % (DK / 8)) * 8;
+      const uint4 u = *reinterpret_cast<const uint4*>((which ? sQ : sK) + r * LD + x);
+      const float s = (which ? sQd : sKd)[r];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = pack_f16x2(__uint_as_float(w[j] << 16) * s, __uint_as_float(w[j] & 0xffff0000u) * s);
+      *reinterpret_cast<uint4*>(K16 + which * L * LD + r * LD + x) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  __syncthreads();
+  // column j of (I + A)^-1: x_i = [i = j] - sum_{l < i} A_il x_l; columns from 32 on start at row 32
+  auto solve = [&](auto first) {
+    constexpr int I0 = decltype(first)::value;
+    float x[L - I0];
+#pragma unroll
+    for (int i = I0; i < L; ++i) {
+      float s[4] = {i == tid ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int l = I0; l < i; l += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(sA + i * 68 + l);
+        s[0] = fmaf(-a.x, x[l - I0], s[0]);
+        if (l + 1 < i) s[1] = fmaf(-a.y, x[l + 1 - I0], s[1]);
+        if (l + 2 < i) s[2] = fmaf(-a.z, x[l + 2 - I0], s[2]);
+        if (l + 3 < i) s[3] = fmaf(-a.w, x[l + 3 - I0], s[3]);
+      }
+      x[i - I0] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    const float b = sB[tid];
+#pragma unroll
+    for (int i = 0; i < L; ++i) sT[i * 65 + tid] = i < I0 ? 0.f : x[i < I0 ? 0 : i - I0] * b;
+  };
+  if (warp == 0) solve(std::integral_constant<int, 0>{});
+  if (warp == 1) solve(std::integral_constant<int, 32>{});
+  __syncthreads();
+  {
+    const int i = tid >> 1, j0 = (tid & 1) * 32;
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(sT[i * 65 + j0 + j]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float down, up;
+    pow2_scale(m, down, up);
+    if ((tid & 1) == 0) scal[DS_T * L + i] = up;
+    __half* T = reinterpret_cast<__half*>(blob) + i * kDeltaLd + j0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        split_f16(sT[i * 65 + j0 + j + 2 * k] * down, sT[i * 65 + j0 + j + 2 * k + 1] * down, hi[k], lo[k]);
+      *reinterpret_cast<uint4*>(T + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(T + L * kDeltaLd + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- chunk after chunk
+// cp.async.bulk of contiguous bytes (16-byte aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+constexpr int kDeltaCols = 128;  // state columns a block (8 warps)
+
+template <int DK>
+struct DeltaChunkCfg {
+  static constexpr int LD = DK + 8;                    // row stride of K, Q
+  static constexpr int KQ = delta_kq_bytes(DK);
+  static constexpr int LDV = kDeltaCols + 8;
+  static constexpr int V = kDeltaL * LDV * 2;
+  static constexpr int STAGE = KQ + kDeltaBlob + V;
+  static constexpr int SMEM = 2 * STAGE + 32;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+// OUT: the outputs and final states of all columns from the right start states.
+// Otherwise: what a part of a sequence adds to the state and does to it, as
+// d_v + d_k columns: the columns of V from a zero state, then, with V = 0, the
+// unit columns, which become the part's transition matrix.
+template <int DK, bool OUT>
+__global__ void __launch_bounds__(256, 1) delta_chunk_kernel(const DeltaChunkParams p, int col_blocks) {
+  pdl_wait();
+  using Cfg = DeltaChunkCfg<DK>;
+  constexpr int L = kDeltaL, LD = Cfg::LD, LDV = Cfg::LDV, NT = DK / 8;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  uint8_t* sm = dsm;
+  const DeltaParams& d = p.d;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + 2 * Cfg::STAGE);  // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
+  const int h = blockIdx.y, hq = h / (d.heads / d.qk_heads);
+  const int cb = blockIdx.x % col_blocks, rest = blockIdx.x / col_blocks;
+  const int segs = OUT ? p.nseg : p.nseg - 1;
+  const int seg = rest % segs, seq = rest / segs;
+  const SeqRows sr = seq_rows(d.offsets, seq, static_cast<int>(d.rows));
+  const int chunks = (sr.len + L - 1) / L, slot0 = sr.begin / L + seq;
+  const int c0 = static_cast<int>(static_cast<long>(chunks) * seg / p.nseg);
+  const int c1 = static_cast<int>(static_cast<long>(chunks) * (seg + 1) / p.nseg);
+  const int cols = OUT ? d.d_v : d.d_v + d.d_k;  // columns of this call
+  const int col0 = cb * kDeltaCols;              // of this block
+  const int vcols = min(max(d.d_v - col0, 0), kDeltaCols);  // of them, columns of V
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  for (int s = 0; s < 2; ++s)  // (columns past V's stay zero)
+    for (int e = tid; e < Cfg::V / 16; e += nthr)
+      *reinterpret_cast<uint4*>(sm + s * Cfg::STAGE + Cfg::KQ + kDeltaBlob + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  // warp 0: chunk c into stage c - c0 mod 2
+  auto load = [&](int c) {
+    uint8_t* st = sm + ((c - c0) & 1) * Cfg::STAGE;
+    uint64_t* bar = &full[(c - c0) & 1];
+    const int n = min(L, sr.len - c * L);
+    __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(st + Cfg::KQ + kDeltaBlob);
+    for (int r = n; r < L; ++r)  // rows behind the sequence: zeros
+      for (int x = lane; x < vcols / 8; x += 32) *reinterpret_cast<uint4*>(v + r * LDV + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+    __syncwarp();
+    const uint32_t kq = OUT ? Cfg::KQ : Cfg::KQ / 2, bl = OUT ? kDeltaBlob : kDeltaBlob - kDeltaMat;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, kq + bl + n * vcols * 2);
+      bulk_load(st, p.kq + (static_cast<long>(slot0 + c) * d.qk_heads + hq) * Cfg::KQ, kq, bar);
+      bulk_load(st + Cfg::KQ, p.blobs + (static_cast<long>(slot0 + c) * d.heads + h) * kDeltaBlob, bl, bar);
+    }
+    __syncwarp();
+    if (vcols > 0)
+      for (int r = lane; r < n; r += 32)
+        bulk_load(v + r * LDV,
+                  static_cast<const __nv_bfloat16*>(d.v) + (sr.begin + static_cast<long>(c) * L + r) * d.ldv + h * d.d_v + col0,
+                  vcols * 2, bar);
+  };
+  if (warp == 0 && c0 < c1) load(c0);
+
+  // S^T of this warp's 16 columns (rows g and g + 8 of the accumulators), by 8 rows of the state
+  const int g = lane >> 2, q2 = 2 * (lane & 3);
+  const int my = col0 + 16 * warp;  // first column
+  float S[NT][4];
+  const long head = static_cast<long>(seq) * d.heads + h;
+  const float* start = nullptr;
+  if (OUT)
+    start = seg == 0 ? (d.state_in ? d.state_in + head * d.d_k * d.d_v : nullptr)
+                     : p.starts + (head * (p.nseg - 1) + seg - 1) * d.d_k * d.d_v;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 8 * t + q2 + (e & 1), j = my + g + 8 * (e >> 1);
+      if (OUT)
+        S[t][e] = start && i < d.d_k && j < d.d_v ? start[static_cast<long>(i) * d.d_v + j] : 0.f;
+      else
+        S[t][e] = j - d.d_v == i ? 1.f : 0.f;
+    }
+
+  // addresses of this lane in ldmatrix's four 8 x 8 blocks
+  const int m_row = (lane & 7) + ((lane >> 4) << 3), m_col = ((lane >> 3) & 1) * 8;  // (n, k) blocks of a row-major B
+  const int t_row = lane & 15, t_col = (lane >> 4) * 8;                              // (k, n) blocks, transposed
+  for (int c = c0; c < c1; ++c) {
+    fence_proxy_async_smem();  // (outputs were staged there)
+    __syncthreads();           // every warp is done with the stage that is loaded next
+    if (warp == 0 && c + 1 < c1) load(c + 1);
+    uint8_t* st = sm + ((c - c0) & 1) * Cfg::STAGE;
+    if (!warp_wait(&full[(c - c0) & 1], ((c - c0) >> 1) & 1, abort_flag, d.status)) break;
+    if (my >= cols) continue;  // (a warp without columns only keeps the block going)
+    const uint32_t sK = smem_u32(st), sQ = sK + Cfg::KQ / 2, sT = sK + Cfg::KQ, sP = sT + 2 * kDeltaMat + kDeltaScal;
+    const float* scal = reinterpret_cast<const float*>(st + Cfg::KQ + 2 * kDeltaMat);
+    const uint32_t sV = sT + kDeltaBlob + 16 * warp * 2;
+
+    // rows of S^T as fp16 halves; X = K S0, Oi = Q S0 (transposed)
+    float mx[2] = {0.f, 0.f}, s_dn[2], s_up[2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], fabsf(S[t][e]));
+    auto row_scale = [&](float (&dn)[2], float (&up)[2]) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        pow2_scale(mx[r], dn[r], up[r]);
+      }
+    };
+    row_scale(s_dn, s_up);
+    float X[8][4] = {}, Oi[OUT ? 8 : 1][4] = {};
+#pragma unroll
+    for (int k = 0; k < DK / 16; ++k) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int t = 2 * k + (b >> 1), r = b & 1;
+        split_f16(S[t][2 * r] * s_dn[r], S[t][2 * r + 1] * s_dn[r], hi[b], lo[b]);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        uint32_t b[4];
+        ldsm_x4(sK + ((16 * t + m_row) * LD + 16 * k + m_col) * 2, b);
+        mma_f16(X[2 * t], hi, b[0], b[1]);
+        mma_f16(X[2 * t + 1], hi, b[2], b[3]);
+        mma_f16(X[2 * t], lo, b[0], b[1]);
+        mma_f16(X[2 * t + 1], lo, b[2], b[3]);
+        if (OUT) {
+          ldsm_x4(sQ + ((16 * t + m_row) * LD + 16 * k + m_col) * 2, b);
+          mma_f16(Oi[OUT ? 2 * t : 0], hi, b[0], b[1]);
+          mma_f16(Oi[OUT ? 2 * t + 1 : 0], hi, b[2], b[3]);
+        }
+      }
+    }
+    // X = V - e^G K^ S0
+    mx[0] = mx[1] = 0.f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {  // 16 tokens
+      uint32_t v[4];
+      // blocks: tokens 16 t + 0..7 / 8..15 (rows) x this warp's columns 0..7 / 8..15, transposed
+      ldsm_x4_t(sV + ((16 * t + (lane & 7) + ((lane >> 4) << 3)) * LDV + ((lane >> 3) & 1) * 8) * 2, v);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float2 fx = *reinterpret_cast<const float2*>(scal + DS_FX * L + 16 * t + 8 * u + q2);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t w = v[2 * u + r];
+          float(&x)[4] = X[2 * t + u];
+          x[2 * r] = fmaf(-x[2 * r], s_up[r] * fx.x, __uint_as_float(w << 16));
+          x[2 * r + 1] = fmaf(-x[2 * r + 1], s_up[r] * fx.y, __uint_as_float(w & 0xffff0000u));
+          mx[r] = fmaxf(mx[r], fmaxf(fabsf(x[2 * r]), fabsf(x[2 * r + 1])));
+        }
+      }
+    }
+    float x_dn[2], x_up[2];
+    row_scale(x_dn, x_up);
+    // U = T X
+    float U[8][4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int t = 2 * k + (b >> 1), r = b & 1;
+        split_f16(X[t][2 * r] * x_dn[r], X[t][2 * r + 1] * x_dn[r], hi[b], lo[b]);
+      }
+#pragma unroll
+      for (int t = k; t < 4; ++t) {  // rows of T from the diagonal block down
+        uint32_t b[4];
+        ldsm_x4(sT + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
+        mma_f16(U[2 * t], hi, b[0], b[1]);
+        mma_f16(U[2 * t + 1], hi, b[2], b[3]);
+        mma_f16(U[2 * t], lo, b[0], b[1]);
+        mma_f16(U[2 * t + 1], lo, b[2], b[3]);
+        ldsm_x4(sT + kDeltaMat + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
+        mma_f16(U[2 * t], hi, b[0], b[1]);
+        mma_f16(U[2 * t + 1], hi, b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float2 f = *reinterpret_cast<const float2*>(scal + DS_T * L + 8 * t + q2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) U[t][e] *= x_up[e >> 1] * (e & 1 ? f.y : f.x);
+    }
+    if (OUT) {
+      // O = Q^ S0 e^G + P U, rounded to bf16, through this warp's columns of V's tile
+      float Op[8][4] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int t = 2 * k + (b >> 1), r = b & 1;
+          a[b] = pack_bf16x2(U[t][2 * r], U[t][2 * r + 1]);
+        }
+#pragma unroll
+        for (int t = k; t < 4; ++t) {
+          uint32_t b[4];
+          ldsm_x4(sP + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
+          mma_bf16(Op[2 * t], a, b[0], b[1]);
+          mma_bf16(Op[2 * t + 1], a, b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        uint32_t o[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float2 fo = *reinterpret_cast<const float2*>(scal + DS_FO * L + 16 * t + 8 * u + q2);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float(&a)[4] = Oi[OUT ? 2 * t + u : 0];
+            const float(&b)[4] = Op[2 * t + u];
+            o[2 * u + r] = pack_bf16x2(fmaf(a[2 * r], s_up[r] * fo.x, b[2 * r]),
+                                       fmaf(a[2 * r + 1], s_up[r] * fo.y, b[2 * r + 1]));
+          }
+        }
+        stsm_x4_t(sV + ((16 * t + (lane & 7) + ((lane >> 4) << 3)) * LDV + ((lane >> 3) & 1) * 8) * 2, o);
+      }
+      __syncwarp();
+      const int n = min(L, sr.len - c * L);
+      const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(st + Cfg::KQ + kDeltaBlob) + 16 * warp;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(d.out) + (sr.begin + static_cast<long>(c) * L) * d.ldo + h * d.d_v + my;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 16 * e + (lane >> 1), x = (lane & 1) * 8;
+        if (r < n && my + x < d.d_v)
+          *reinterpret_cast<uint4*>(out + r * d.ldo + x) = *reinterpret_cast<const uint4*>(v + r * LDV + x);
+      }
+    }
+    // S = e^G_64 S + (e^(G_64 - G) K^)^T U
+    mx[0] = mx[1] = 0.f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float2 f = *reinterpret_cast<const float2*>(scal + DS_W * L + 8 * t + q2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        U[t][e] *= e & 1 ? f.y : f.x;
+        mx[e >> 1] = fmaxf(mx[e >> 1], fabsf(U[t][e]));
+      }
+    }
+    float w_dn[2], w_up[2];
+    row_scale(w_dn, w_up);
+    uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int t = 2 * k + (b >> 1), r = b & 1;
+        split_f16(U[t][2 * r] * w_dn[r], U[t][2 * r + 1] * w_dn[r], hi[k][b], lo[k][b]);
+      }
+    const float a = scal[DS_A * L];
+#pragma unroll
+    for (int t = 0; t < NT; t += 2) {
+      float D[2][4] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t b[4];
+        ldsm_x4_t(sK + ((16 * k + t_row) * LD + 8 * t + t_col) * 2, b);
+        mma_f16(D[0], hi[k], b[0], b[1]);
+        mma_f16(D[1], hi[k], b[2], b[3]);
+        mma_f16(D[0], lo[k], b[0], b[1]);
+        mma_f16(D[1], lo[k], b[2], b[3]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t + u][e] = fmaf(D[u][e], w_up[e >> 1], a * S[t + u][e]);
+    }
+  }
+
+  float* end = nullptr;
+  if (OUT) {
+    if (d.state_out && seg == p.nseg - 1) end = d.state_out + head * d.d_k * d.d_v;
+  } else {
+    end = p.trans + (head * (p.nseg - 1) + seg) * d.d_k * cols;
+  }
+  if (end) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 8 * t + q2 + (e & 1), j = my + g + 8 * (e >> 1);
+        if (i < d.d_k && j < cols) end[static_cast<long>(i) * cols + j] = S[t][e];
+      }
+  }
+}
+
+// The state before each part: starts[0] = B_0 + M_0 state_in, starts[s] = B_s +
+// M_s starts[s - 1] (fp32 products). One block for 32 columns of one (sequence,
+// head); 256 threads, 4 x 4 values each (DK = 128), M^T staged in shared memory.
+template <int DK>
+__global__ void __launch_bounds__(DK * 2) delta_join_kernel(const DeltaChunkParams p) {
+  pdl_wait();
+  extern __shared__ __align__(128) uint8_t dsm[];
+  uint8_t* sm = dsm;
+  const DeltaParams& d = p.d;
+  float* sMt = reinterpret_cast<float*>(sm);  // [DK (k)][DK + 4 (row)]
+  float* sS = sMt + DK * (DK + 4);            // [DK][32]
+  const int h = blockIdx.y, seq = blockIdx.z, col0 = blockIdx.x * 32;
+  const long head = static_cast<long>(seq) * d.heads + h;
+  const int cols = d.d_v + d.d_k, tid = threadIdx.x;
+  const int r0 = (tid >> 3) * 4, x0 = (tid & 7) * 4;  // this thread's rows and columns
+  for (int e = tid; e < DK * 32; e += DK * 2) {
+    const int i = e >> 5, j = col0 + (e & 31);
+    sS[e] = d.state_in && i < d.d_k && j < d.d_v ? d.state_in[(head * d.d_k + i) * d.d_v + j] : 0.f;
+  }
+  for (int s = 0; s + 1 < p.nseg; ++s) {
+    const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols;
+    for (int e = tid; e < DK * DK; e += DK * 2) {
+      const int i = e / DK, k = e % DK;
+      sMt[k * (DK + 4) + i] = i < d.d_k && k < d.d_k ? tr[static_cast<long>(i) * cols + d.d_v + k] : 0.f;
+    }
+    __syncthreads();
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = r0 + i < d.d_k && col0 + x0 + j < d.d_v ? tr[static_cast<long>(r0 + i) * cols + col0 + x0 + j] : 0.f;
+#pragma unroll 4
+    for (int k = 0; k < DK; ++k) {
+      const float4 m = *reinterpret_cast<const float4*>(sMt + k * (DK + 4) + r0);
+      const float4 v = *reinterpret_cast<const float4*>(sS + k * 32 + x0);
+      const float mi[4] = {m.x, m.y, m.z, m.w}, vj[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(mi[i], vj[j], acc[i][j]);
+    }
+    __syncthreads();
+    float* to = p.starts + (head * (p.nseg - 1) + s) * d.d_k * d.d_v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sS[(r0 + i) * 32 + x0 + j] = acc[i][j];
+        if (r0 + i < d.d_k && col0 + x0 + j < d.d_v) to[static_cast<long>(r0 + i) * d.d_v + col0 + x0 + j] = acc[i][j];
+      }
+  }
+}
+
+}  // namespace edit

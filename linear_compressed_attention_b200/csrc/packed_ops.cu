@@ -11,6 +11,7 @@
 
 #include "block_norm.cuh"
 #include "common.cuh"
+#include "delta_chunk.cuh"
 #include "delta_rule.cuh"
 #include "host.h"
 #include "packed_attn.cuh"
@@ -159,6 +160,8 @@ int attn_run(PackedAttnParams p, int row_tiles, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------ delta rule
+constexpr int kDeltaMaxSeg = 16;  // most parts of a sequence (delta_nseg)
+
 int delta_args(const edit_delta_rule* a, bool step) {
   if (!a) return EDIT_ERR_NULL;
   if (a->dtype != EDIT_F32 && a->dtype != EDIT_BF16) return EDIT_ERR_DTYPE;
@@ -168,7 +171,7 @@ int delta_args(const edit_delta_rule* a, bool step) {
   if (a->d_k % 8 != 0 || a->d_k > 128 || a->d_v % 8 != 0 || a->d_v > 256 || a->heads > 65535)
     return EDIT_ERR_UNSUPPORTED;
   if (!step && a->rows > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
-  if (static_cast<long>(a->nseq) * 4 > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (static_cast<long>(a->nseq) * 4 * kDeltaMaxSeg > INT32_MAX || (!step && a->nseq > 65535)) return EDIT_ERR_UNSUPPORTED;
   return EDIT_OK;
 }
 
@@ -221,6 +224,75 @@ int delta_recurrent(const DeltaParams& p, cudaStream_t st) {
   if (p.d_k <= 64) return launch(delta_recurrent_kernel<T, 64>, grid, block, 0, st, p, cb);
   if (p.d_k <= 96) return launch(delta_recurrent_kernel<T, 96>, grid, block, 0, st, p, cb);
   return launch(delta_recurrent_kernel<T, 128>, grid, block, 0, st, p, cb);
+}
+
+// bf16 calls with sequences of at least this many rows on average run in chunks
+// of 64 tokens, others token by token.
+constexpr int kDeltaChunkedRows = 32;
+
+struct DeltaPlan {
+  bool chunked;
+  int DK, slots, nseg;
+  size_t blobs, kq, trans, starts, total;
+};
+
+// Parts each sequence's chunks are cut into: with few (sequence, head) pairs the
+// walk over the chunks leaves SMs idle. A part's effect is found first (pass 1,
+// on d_v + d_k columns), joined part after part (about 1.5 chunks' time each),
+// then the parts run side by side (pass 2). The number with the least time, in
+// chunks.
+int delta_nseg(const edit_delta_rule* a, int64_t chunks, int sms) {
+  const int64_t heads = static_cast<int64_t>(a->nseq) * a->heads;
+  const int64_t b1 = heads * ceil_div(a->d_v + a->d_k, kDeltaCols), b2 = heads * ceil_div(a->d_v, kDeltaCols);
+  int best = 1;
+  double least = static_cast<double>(ceil_div(b2, sms)) * chunks;
+  for (int n = 2; n <= kDeltaMaxSeg; ++n) {
+    const double t = static_cast<double>(ceil_div(b1 * (n - 1), sms) + ceil_div(b2 * n, sms)) * ceil_div(chunks, n) + 1.5 * n;
+    if (t < 0.9 * least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
+void delta_plan(const edit_delta_rule* a, DeltaPlan& pl) {
+  pl = DeltaPlan{};
+  pl.total = kStatusBytes;
+  pl.chunked = a->dtype == EDIT_BF16 && a->rows >= static_cast<int64_t>(kDeltaChunkedRows) * a->nseq;
+  if (!pl.chunked) return;
+  pl.DK = a->d_k <= 64 ? 64 : 128;
+  pl.slots = static_cast<int>(a->rows / kDeltaL + a->nseq);
+  pl.nseg = delta_nseg(a, ceil_div(a->rows, static_cast<int64_t>(kDeltaL) * a->nseq), device_sms());
+  const size_t heads = static_cast<size_t>(a->nseq) * a->heads;
+  auto take = [&](size_t bytes) {
+    const size_t at = pl.total;
+    pl.total += align256(bytes);
+    return at;
+  };
+  pl.blobs = take(static_cast<size_t>(pl.slots) * a->heads * kDeltaBlob);
+  pl.kq = take(static_cast<size_t>(pl.slots) * a->qk_heads * delta_kq_bytes(pl.DK));
+  pl.trans = take(heads * (pl.nseg - 1) * a->d_k * (a->d_v + a->d_k) * 4);
+  pl.starts = take(heads * (pl.nseg - 1) * a->d_k * a->d_v * 4);
+}
+
+template <int DK>
+int delta_chunked(const DeltaChunkParams& p, cudaStream_t st) {
+  const DeltaParams& d = p.d;
+  EDIT_TRY(launch(delta_prep_kernel<DK>, dim3(p.slots, d.heads), dim3(128), DeltaPrepCfg<DK>::SMEM, st, p));
+  auto blocks = [&](int cols, int parts) {
+    return dim3(static_cast<unsigned>(ceil_div(cols, kDeltaCols) * parts * d.nseq), d.heads);
+  };
+  auto warps = [](int cols) { return dim3(static_cast<unsigned>(32 * ceil_div(cols < kDeltaCols ? cols : kDeltaCols, 16))); };
+  if (p.nseg > 1) {
+    const int cols = d.d_v + d.d_k;
+    EDIT_TRY(launch(delta_chunk_kernel<DK, false>, blocks(cols, p.nseg - 1), warps(cols), DeltaChunkCfg<DK>::SMEM, st, p,
+                    static_cast<int>(ceil_div(cols, kDeltaCols))));
+    EDIT_TRY(launch(delta_join_kernel<DK>, dim3(static_cast<unsigned>(ceil_div(d.d_v, 32)), d.heads, d.nseq), dim3(DK * 2),
+                    (DK * (DK + 4) + DK * 32) * sizeof(float), st, p));
+  }
+  return launch(delta_chunk_kernel<DK, true>, blocks(d.d_v, p.nseg), warps(d.d_v), DeltaChunkCfg<DK>::SMEM, st, p,
+                static_cast<int>(ceil_div(d.d_v, kDeltaCols)));
 }
 
 // ------------------------------------------------------------ block norm
@@ -317,7 +389,19 @@ int edit_packed_attention_forward(const void* q, const void* k, const void* v, c
 
 size_t edit_delta_rule_workspace_bytes(const edit_delta_rule* a) {
   if (delta_args(a, false) != EDIT_OK) return 0;
-  return kStatusBytes;
+  // Fewer rows take fewer slots, but can take more parts: room for the most parts of
+  // any row count.
+  DeltaPlan pl;
+  delta_plan(a, pl);
+  if (!pl.chunked) return pl.total;
+  const int64_t chunks = ceil_div(a->rows, static_cast<int64_t>(kDeltaL) * a->nseq);
+  int most = 1;
+  for (int64_t c = chunks < 1024 ? chunks : 1024; c >= 1; --c) {
+    const int n = delta_nseg(a, c, device_sms());
+    most = n > most ? n : most;
+  }
+  const size_t heads = static_cast<size_t>(a->nseq) * a->heads, more = most > pl.nseg ? most - pl.nseg : 0;
+  return pl.total + align256(heads * more * a->d_k * (a->d_v + a->d_k) * 4) + align256(heads * more * a->d_k * a->d_v * 4);
 }
 
 int edit_delta_rule_forward(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -328,13 +412,27 @@ int edit_delta_rule_forward(const void* q, const void* k, const void* v, const f
   if (!a->offsets || !a->workspace) return EDIT_ERR_NULL;
   if (!aligned(a->workspace, 256) || !aligned(a->offsets, 4) || !aligned(state_in, 16) || !aligned(state_out, 16))
     return EDIT_ERR_ALIGN;
-  if (a->workspace_bytes < kStatusBytes) return EDIT_ERR_WORKSPACE;
+  DeltaPlan pl;
+  delta_plan(a, pl);
+  if (a->workspace_bytes < pl.total) return EDIT_ERR_WORKSPACE;
   DeltaParams p = delta_params(q, k, v, g, beta, a, out);
   p.offsets = a->offsets;
   p.state_in = state_in;
   p.state_out = state_out;
   p.status = static_cast<int*>(a->workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (pl.chunked) {
+    uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+    DeltaChunkParams c = {};
+    c.d = p;
+    c.blobs = ws + pl.blobs;
+    c.kq = ws + pl.kq;
+    c.slots = pl.slots;
+    c.nseg = pl.nseg;
+    c.trans = reinterpret_cast<float*>(ws + pl.trans);
+    c.starts = reinterpret_cast<float*>(ws + pl.starts);
+    return pl.DK == 64 ? delta_chunked<64>(c, st) : delta_chunked<128>(c, st);
+  }
   return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16>(p, st) : delta_recurrent<float>(p, st);
 }
 
