@@ -107,13 +107,22 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 
 // ---------------------------------------------------------------- chunks by themselves
 // One block a (chunk, head). Warp w forms rows 16 w .. 16 w + 15 of K K^T and
-// Q K^T (exact bf16 products, fp32 sums); thread j < 64 then solves column j of
-// the unit triangular system by forward substitution in registers.
+// Q K^T (exact bf16 products, fp32 sums). The unit triangular matrix is inverted
+// in fp32 by blocks: four 16 x 16 blocks by forward substitution, one column a
+// thread, then twice (I + A)^-1_21 = -T22 A21 T11 with small register tiles. (All
+// 64 columns by forward substitution, unrolled, took 125 us for 2064 chunks and
+// heads of 128, most of it fetching instructions.)
 template <int DK>
 struct DeltaPrepCfg {
   static constexpr int LD = DK + 8;
-  static constexpr int SMEM = 2 * kDeltaL * LD * 2 + kDeltaL * 68 * 4 + kDeltaL * 65 * 4 + kDeltaL * 8 + 8 * kDeltaL * 4;
+  static constexpr int KQ = 2 * kDeltaL * LD * 2, AT = 2 * kDeltaL * 68 * 4;
+  static constexpr int SMEM = (KQ > AT ? KQ : AT) + 11 * kDeltaL * 4;  // K and Q, later A and T; rows of scalars
 };
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool real) {  // zeros where not real
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
+               : "memory");
+}
 
 template <int DK>
 __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams p) {
@@ -121,18 +130,18 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams 
   const DeltaParams& d = p.d;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     check_offsets(d.offsets, d.rows, nullptr, 0, nullptr, 0, d.nseq, d.status);
-  constexpr int L = kDeltaL, LD = DeltaPrepCfg<DK>::LD;
+  using Cfg = DeltaPrepCfg<DK>;
+  constexpr int L = kDeltaL, LD = Cfg::LD;
   extern __shared__ __align__(128) uint8_t dsm[];
-  uint8_t* sm = dsm;
-  __nv_bfloat16* sK = reinterpret_cast<__nv_bfloat16*>(sm);
+  __nv_bfloat16* sK = reinterpret_cast<__nv_bfloat16*>(dsm);
   __nv_bfloat16* sQ = sK + L * LD;
-  float* sA = reinterpret_cast<float*>(sQ + L * LD);  // [64][68]
-  float* sT = sA + L * 68;                            // [64][65]
-  double* sG = reinterpret_cast<double*>(sT + L * 65);
-  float* sRk = reinterpret_cast<float*>(sG + L);
-  float *sRq = sRk + L, *sKd = sRq + L, *sKu = sKd + L, *sQd = sKu + L, *sQu = sQd + L, *sB = sQu + L;
+  float* sA = reinterpret_cast<float*>(dsm);  // [64][68], over K and Q
+  float* sT = sA + L * 68;                    // [64][68]
+  float* sGh = reinterpret_cast<float*>(dsm + Cfg::SMEM - 11 * L * 4);  // running sum of g: high and low part
+  float *sGl = sGh + L, *sB = sGl + L, *sRk = sB + L, *sRq = sRk + L, *sKd = sRq + L, *sKu = sKd + L, *sQd = sKu + L,
+        *sQu = sQd + L, *sNk = sQu + L, *sNq = sNk + L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slot = blockIdx.x, h = blockIdx.y, hq = h / (d.heads / d.qk_heads);
+  const int slot = blockIdx.x, h = blockIdx.y, share = d.heads / d.qk_heads, hq = h / share;
   const int seq = seq_of_slot(d.offsets, d.nseq, static_cast<int>(d.rows), L, slot);
   const SeqRows sr = seq_rows(d.offsets, seq, static_cast<int>(d.rows));
   const int c = slot - (sr.begin / L + seq);
@@ -140,68 +149,54 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams 
   const int n = min(L, sr.len - c * L);
   const long row0 = sr.begin + static_cast<long>(c) * L;
 
-  for (int e = tid; e < L * (DK / 8); e += 128) {
-    const int r = e / (DK / 8), x = (e % (DK / 8)) * 8;
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), q = k;
-    if (r < n && x < d.d_k) {
-      k = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.k) + (row0 + r) * d.ldk + hq * d.d_k + x);
-      q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.q) + (row0 + r) * d.ldq + hq * d.d_k + x);
+  {
+    const __nv_bfloat16* kg = static_cast<const __nv_bfloat16*>(d.k) + row0 * d.ldk + hq * d.d_k;
+    const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(d.q) + row0 * d.ldq + hq * d.d_k;
+#pragma unroll
+    for (int e = tid; e < L * (DK / 8); e += 128) {
+      const int r = e / (DK / 8), x = (e % (DK / 8)) * 8;
+      const bool real = r < n && x < d.d_k;
+      cp_async16(sK + r * LD + x, real ? kg + r * d.ldk + x : kg, real);
+      cp_async16(sQ + r * LD + x, real ? qg + r * d.ldq + x : qg, real);
     }
-    *reinterpret_cast<uint4*>(sK + r * LD + x) = k;
-    *reinterpret_cast<uint4*>(sQ + r * LD + x) = q;
   }
+  double G = 0.0;
   if (tid < L) {  // running sums of g in fp64: differences of far sums keep their fp32 precision
-    double G = tid < n ? static_cast<double>(log_decay(d.g[(row0 + tid) * d.ldg + h])) : 0.0;
+    if (tid < n) G = static_cast<double>(log_decay(d.g[(row0 + tid) * d.ldg + h]));
+    sB[tid] = tid < n ? d.beta[(row0 + tid) * d.ldb + h] : 0.f;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double a = __shfl_up_sync(0xffffffffu, G, o);
       if (lane >= o) G += a;
     }
-    sG[tid] = G;
-    sB[tid] = tid < n ? d.beta[(row0 + tid) * d.ldb + h] : 0.f;
-  }
-  __syncthreads();
-  {
-    const int t = tid & 63;
-    const __nv_bfloat16* x = (tid < 64 ? sK : sQ) + t * LD;
-    float s = 0.f, m = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < DK; i += 8) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
-        s = fmaf(a, a, fmaf(b, b, s));
-        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
-      }
+    if (tid == 31) {
+      sGh[0] = static_cast<float>(G);
+      sGl[0] = static_cast<float>(G - static_cast<double>(sGh[0]));
     }
-    float down, up;
-    pow2_scale(m, down, up);
-    const float r = t >= n ? 0.f : (d.qk_norm ? 1.f / sqrtf(s + d.qk_eps) : 1.f);
-    (tid < 64 ? sRk : sRq)[t] = r;
-    (tid < 64 ? sKd : sQd)[t] = down;
-    (tid < 64 ? sKu : sQu)[t] = up;
-    if (tid >= 32 && tid < 64) sG[tid] += sG[31];
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if (warp == 1) G += static_cast<double>(sGh[0]) + static_cast<double>(sGl[0]);
   uint8_t* blob = p.blobs + (static_cast<long>(slot) * d.heads + h) * kDeltaBlob;
   float* scal = reinterpret_cast<float*>(blob + 2 * kDeltaMat);
+  // K K^T and Q K^T of this warp's 16 rows, columns up to its diagonal block; |q|^2 from the diagonal of Q Q^T
+  const int gr = lane >> 2, q2 = 2 * (lane & 3);
+  float kk[8][4] = {}, qk[8][4] = {}, qq[2][4] = {};
   {
-    // K K^T and Q K^T of this warp's 16 rows, columns up to its diagonal block
-    float kk[8][4] = {}, qk[8][4] = {};
     const uint32_t ka = smem_u32(sK), qa = smem_u32(sQ);
     const uint32_t arow = (16 * warp + (lane & 15)) * LD * 2 + (lane >> 4) * 16;
     const uint32_t brow = ((lane & 7) + ((lane >> 4) << 3)) * LD * 2 + ((lane >> 3) & 1) * 16;
 #pragma unroll
     for (int k = 0; k < DK / 16; ++k) {
-      uint32_t a[4], q[4];
+      uint32_t a[4], q[4], b[4];
       ldsm_x4(ka + arow + 32 * k, a);
       ldsm_x4(qa + arow + 32 * k, q);
+      ldsm_x4(qa + brow + warp * 16 * LD * 2 + 32 * k, b);
+      mma_bf16(qq[0], q, b[0], b[1]);
+      mma_bf16(qq[1], q, b[2], b[3]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         if (t > warp) break;
-        uint32_t b[4];
         ldsm_x4(ka + brow + t * 16 * LD * 2 + 32 * k, b);
         mma_bf16(kk[2 * t], a, b[0], b[1]);
         mma_bf16(kk[2 * t + 1], a, b[2], b[3]);
@@ -209,76 +204,150 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams 
         mma_bf16(qk[2 * t + 1], q, b[2], b[3]);
       }
     }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)  // diagonal: row gr (+ 8) of the block in its first (second) 8 columns
+      if (t == warp) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (q2 + e == gr) {
+            sNk[16 * t + gr] = kk[2 * t][e];
+            sNk[16 * t + gr + 8] = kk[2 * t + 1][2 + e];
+            sNq[16 * t + gr] = qq[0][e];
+            sNq[16 * t + gr + 8] = qq[1][2 + e];
+          }
+      }
+  }
+  __syncthreads();
+  {
+    const int t = tid & 63;
+    const float s = (tid < 64 ? sNk : sNq)[t];
+    float down, up;
+    pow2_scale(sqrtf(s), down, up);  // (no value is larger than the norm)
+    (tid < 64 ? sRk : sRq)[t] = t >= n ? 0.f : (d.qk_norm ? 1.f / sqrtf(s + d.qk_eps) : 1.f);
+    (tid < 64 ? sKd : sQd)[t] = down;
+    (tid < 64 ? sKu : sQu)[t] = up;
+    if (tid < 64) {
+      const float hi = static_cast<float>(G);
+      sGh[tid] = hi;
+      sGl[tid] = static_cast<float>(G - static_cast<double>(hi));
+    }
+  }
+  __syncthreads();
+  if (tid < L) {
+    const float eG = expf(sGh[tid]), rest = expf((sGh[L - 1] - sGh[tid]) + (sGl[L - 1] - sGl[tid]));
+    scal[DS_FX * L + tid] = eG * sRk[tid] * sKu[tid];
+    scal[DS_W * L + tid] = rest * sRk[tid] * sKu[tid];
+    scal[DS_FO * L + tid] = d.scale * eG * sRq[tid] * sQu[tid];
+    scal[DS_A * L + tid] = expf(sGh[L - 1]);
+  }
+  {
     __nv_bfloat16* P = reinterpret_cast<__nv_bfloat16*>(blob + 2 * kDeltaMat + kDeltaScal);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       if (t > 2 * warp + 1) break;
+      const int j = 8 * t + q2;
+      const float2 gh = *reinterpret_cast<const float2*>(sGh + j), gl = *reinterpret_cast<const float2*>(sGl + j),
+                   rk = *reinterpret_cast<const float2*>(sRk + j);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int i = 16 * warp + (lane >> 2) + 8 * r, j0 = 8 * t + 2 * (lane & 3);
-        float pv[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = j0 + e;
-          const float gam = j <= i ? expf(static_cast<float>(sG[i] - sG[j])) * sRk[j] : 0.f;
-          sA[i * 68 + j] = j < i ? sB[i] * sRk[i] * gam * kk[t][2 * r + e] : 0.f;
-          pv[e] = j <= i ? d.scale * gam * sRq[i] * qk[t][2 * r + e] : 0.f;
-        }
-        *reinterpret_cast<uint32_t*>(P + i * kDeltaLd + j0) = pack_bf16x2(pv[0], pv[1]);
+        const int i = 16 * warp + gr + 8 * r;
+        const float hi = sGh[i], lo = sGl[i], bk = sB[i] * sRk[i], rq = d.scale * sRq[i];
+        const float g0 = j <= i ? expf((hi - gh.x) + (lo - gl.x)) * rk.x : 0.f;
+        const float g1 = j + 1 <= i ? expf((hi - gh.y) + (lo - gl.y)) * rk.y : 0.f;
+        kk[t][2 * r] = j < i ? bk * g0 * kk[t][2 * r] : 0.f;
+        kk[t][2 * r + 1] = j + 1 < i ? bk * g1 * kk[t][2 * r + 1] : 0.f;
+        *reinterpret_cast<uint32_t*>(P + i * kDeltaLd + j) =
+            pack_bf16x2(j <= i ? g0 * rq * qk[t][2 * r] : 0.f, j + 1 <= i ? g1 * rq * qk[t][2 * r + 1] : 0.f);
       }
     }
   }
-  if (tid < L) {
-    const float eG = expf(static_cast<float>(sG[tid])), rest = expf(static_cast<float>(sG[L - 1] - sG[tid]));
-    scal[DS_FX * L + tid] = eG * sRk[tid] * sKu[tid];
-    scal[DS_W * L + tid] = rest * sRk[tid] * sKu[tid];
-    scal[DS_FO * L + tid] = d.scale * eG * sRq[tid] * sQu[tid];
-    scal[DS_A * L + tid] = expf(static_cast<float>(sG[L - 1]));
-  }
-  if (h % (d.heads / d.qk_heads) == 0) {  // fp16 K and Q for all heads that share them
+  if (h % share == 0) {  // fp16 K and Q for all heads that share them
     __half* K16 = reinterpret_cast<__half*>(p.kq + (static_cast<long>(slot) * d.qk_heads + hq) * delta_kq_bytes(DK));
+#pragma unroll 4
     for (int e = tid; e < 2 * L * (DK / 8); e += 128) {
-      const int which = e / (L * (DK / 8)), f = e % (L * (DK / 8)), r = f / (DK / 8), x = (f % (DK / 8)) * 8;
-      const uint4 u = *reinterpret_cast<const uint4*>((which ? sQ : sK) + r * LD + x);
-      const float s = (which ? sQd : sKd)[r];
+      const int r = e / (DK / 8), x = (e % (DK / 8)) * 8;  // rows of K, then of Q
+      const uint4 u = *reinterpret_cast<const uint4*>(sK + r * LD + x);
+      const float s = r < L ? sKd[r] : sQd[r - L];
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         o[j] = pack_f16x2(__uint_as_float(w[j] << 16) * s, __uint_as_float(w[j] & 0xffff0000u) * s);
-      *reinterpret_cast<uint4*>(K16 + which * L * LD + r * LD + x) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(K16 + r * LD + x) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  __syncthreads();  // K and Q are done with
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    if (t > 2 * warp + 1) break;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      *reinterpret_cast<float2*>(sA + (16 * warp + gr + 8 * r) * 68 + 8 * t + q2) =
+          make_float2(kk[t][2 * r], kk[t][2 * r + 1]);
+  }
+  for (int e = tid; e < L * 17; e += 128) *reinterpret_cast<float4*>(sT + 4 * e) = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  if (tid < L) {  // diagonal blocks, column tid: x_i = [i = j] - sum_{l < i} A_il x_l
+    const int o = tid & ~15, j = tid & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0 = i == j ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+      for (int l = 0; l < i; ++l) {
+        const float a = sA[(o + i) * 68 + o + l];
+        if (l & 1)
+          s1 = fmaf(-a, x[l], s1);
+        else
+          s0 = fmaf(-a, x[l], s0);
+      }
+      x[i] = s0 + s1;
+      sT[(o + i) * 68 + tid] = x[i];
     }
   }
   __syncthreads();
-  // column j of (I + A)^-1: x_i = [i = j] - sum_{l < i} A_il x_l; columns from 32 on start at row 32
-  auto solve = [&](auto first) {
-    constexpr int I0 = decltype(first)::value;
-    float x[L - I0];
+  // rows o2 .. o2 + N - 1, columns o1 .. o1 + N - 1 of the inverse, o2 = o1 + N: first A21 T11, then -T22 of it; a
+  // thread holds RT rows x 4 columns
+  auto merge = [&](auto size, auto rows, int o1, int u) {
+    constexpr int N = decltype(size)::value, RT = decltype(rows)::value;
+    const int o2 = o1 + N, r = (u / (N / 4)) * RT, x = (u % (N / 4)) * 4;
+    float y[RT][4];
+    auto product = [&](const float* A, const float* B) {
 #pragma unroll
-    for (int i = I0; i < L; ++i) {
-      float s[4] = {i == tid ? 1.f : 0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < RT; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < N; ++k) {
+        const float4 b = *reinterpret_cast<const float4*>(B + k * 68 + x);
 #pragma unroll
-      for (int l = I0; l < i; l += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(sA + i * 68 + l);
-        s[0] = fmaf(-a.x, x[l - I0], s[0]);
-        if (l + 1 < i) s[1] = fmaf(-a.y, x[l + 1 - I0], s[1]);
-        if (l + 2 < i) s[2] = fmaf(-a.z, x[l + 2 - I0], s[2]);
-        if (l + 3 < i) s[3] = fmaf(-a.w, x[l + 3 - I0], s[3]);
+        for (int i = 0; i < RT; ++i) {
+          const float a = A[(r + i) * 68 + k];
+          y[i][0] = fmaf(a, b.x, y[i][0]);
+          y[i][1] = fmaf(a, b.y, y[i][1]);
+          y[i][2] = fmaf(a, b.z, y[i][2]);
+          y[i][3] = fmaf(a, b.w, y[i][3]);
+        }
       }
-      x[i - I0] = (s[0] + s[1]) + (s[2] + s[3]);
-    }
-    const float b = sB[tid];
+    };
+    float* to = sT + o2 * 68 + o1;
+    product(sA + o2 * 68 + o1, sT + o1 * 68 + o1);
 #pragma unroll
-    for (int i = 0; i < L; ++i) sT[i * 65 + tid] = i < I0 ? 0.f : x[i < I0 ? 0 : i - I0] * b;
+    for (int i = 0; i < RT; ++i)
+      *reinterpret_cast<float4*>(to + (r + i) * 68 + x) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
+    __syncthreads();
+    product(sT + o2 * 68 + o2, to);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      *reinterpret_cast<float4*>(to + (r + i) * 68 + x) = make_float4(-y[i][0], -y[i][1], -y[i][2], -y[i][3]);
+    __syncthreads();
   };
-  if (warp == 0) solve(std::integral_constant<int, 0>{});
-  if (warp == 1) solve(std::integral_constant<int, 32>{});
-  __syncthreads();
+  merge(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, 32 * (tid >> 6), tid & 63);
+  merge(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{}, 0, tid);
   {
     const int i = tid >> 1, j0 = (tid & 1) * 32;
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(sT[i * 65 + j0 + j]));
+    for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(sT[i * 68 + j0 + j] * sB[j0 + j]));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     float down, up;
     pow2_scale(m, down, up);
@@ -289,7 +358,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams 
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        split_f16(sT[i * 65 + j0 + j + 2 * k] * down, sT[i * 65 + j0 + j + 2 * k + 1] * down, hi[k], lo[k]);
+        split_f16(sT[i * 68 + j0 + j + 2 * k] * sB[j0 + j + 2 * k] * down,
+                  sT[i * 68 + j0 + j + 2 * k + 1] * sB[j0 + j + 2 * k + 1] * down, hi[k], lo[k]);
       *reinterpret_cast<uint4*>(T + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(T + L * kDeltaLd + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
@@ -308,14 +378,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 constexpr int kDeltaCols = 128;  // state columns a block (8 warps)
 
 template <int DK>
-struct DeltaChunkCfg {
-  static constexpr int LD = DK + 8;                    // row stride of K, Q
+struct DeltaChunkCfg {  // two stages of K, Q, a blob and V's columns of `warps` warps
+  static constexpr int LD = DK + 8;  // row stride of K, Q
   static constexpr int KQ = delta_kq_bytes(DK);
-  static constexpr int LDV = kDeltaCols + 8;
-  static constexpr int V = kDeltaL * LDV * 2;
-  static constexpr int STAGE = KQ + kDeltaBlob + V;
-  static constexpr int SMEM = 2 * STAGE + 32;
-  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int stage(int warps) { return KQ + kDeltaBlob + kDeltaL * (16 * warps + 8) * 2; }
+  static constexpr int smem(int warps) { return 2 * stage(warps) + 64; }
+  static_assert(smem(8) <= 232448, "shared memory");
 };
 
 // OUT: the outputs and final states of all columns from the right start states.
@@ -323,15 +391,18 @@ struct DeltaChunkCfg {
 // d_v + d_k columns: the columns of V from a zero state, then, with V = 0, the
 // unit columns, which become the part's transition matrix.
 template <int DK, bool OUT>
-__global__ void __launch_bounds__(256, 1) delta_chunk_kernel(const DeltaChunkParams p, int col_blocks) {
+__global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkParams p, int col_blocks) {
   pdl_wait();
   using Cfg = DeltaChunkCfg<DK>;
-  constexpr int L = kDeltaL, LD = Cfg::LD, LDV = Cfg::LDV, NT = DK / 8;
+  constexpr int L = kDeltaL, LD = Cfg::LD, NT = DK / 8;
+  const int workers = blockDim.x / 32 - 1;  // warps with 16 columns each; the last warp loads
+  const int LDV = 16 * workers + 8, STAGE = Cfg::KQ + kDeltaBlob + L * LDV * 2;
   extern __shared__ __align__(128) uint8_t dsm[];
   uint8_t* sm = dsm;
   const DeltaParams& d = p.d;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + 2 * Cfg::STAGE);  // [2]
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + 2);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + 2 * STAGE);  // [2]
+  uint64_t* empty = full + 2;                                     // [2]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
   const int h = blockIdx.y, hq = h / (d.heads / d.qk_heads);
   const int cb = blockIdx.x % col_blocks, rest = blockIdx.x / col_blocks;
@@ -347,38 +418,45 @@ __global__ void __launch_bounds__(256, 1) delta_chunk_kernel(const DeltaChunkPar
   if (tid == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
+    mbar_init(&empty[0], workers);
+    mbar_init(&empty[1], workers);
     *abort_flag = 0;
     fence_mbar_init();
   }
   for (int s = 0; s < 2; ++s)  // (columns past V's stay zero)
-    for (int e = tid; e < Cfg::V / 16; e += nthr)
-      *reinterpret_cast<uint4*>(sm + s * Cfg::STAGE + Cfg::KQ + kDeltaBlob + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int e = tid; e < L * LDV / 8; e += nthr)
+      *reinterpret_cast<uint4*>(sm + s * STAGE + Cfg::KQ + kDeltaBlob + e * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncthreads();
 
-  // warp 0: chunk c into stage c - c0 mod 2
-  auto load = [&](int c) {
-    uint8_t* st = sm + ((c - c0) & 1) * Cfg::STAGE;
-    uint64_t* bar = &full[(c - c0) & 1];
-    const int n = min(L, sr.len - c * L);
-    __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(st + Cfg::KQ + kDeltaBlob);
-    for (int r = n; r < L; ++r)  // rows behind the sequence: zeros
-      for (int x = lane; x < vcols / 8; x += 32) *reinterpret_cast<uint4*>(v + r * LDV + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
-    __syncwarp();
-    const uint32_t kq = OUT ? Cfg::KQ : Cfg::KQ / 2, bl = OUT ? kDeltaBlob : kDeltaBlob - kDeltaMat;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, kq + bl + n * vcols * 2);
-      bulk_load(st, p.kq + (static_cast<long>(slot0 + c) * d.qk_heads + hq) * Cfg::KQ, kq, bar);
-      bulk_load(st + Cfg::KQ, p.blobs + (static_cast<long>(slot0 + c) * d.heads + h) * kDeltaBlob, bl, bar);
+  if (warp == workers) {
+    // ------------------------------------------------------------ loads: chunk c into stage c - c0 mod 2
+    for (int c = c0; c < c1; ++c) {
+      uint8_t* st = sm + ((c - c0) & 1) * STAGE;
+      uint64_t* bar = &full[(c - c0) & 1];
+      if (!warp_wait(&empty[(c - c0) & 1], (((c - c0) >> 1) & 1) ^ 1, abort_flag, d.status)) break;
+      const int n = min(L, sr.len - c * L);
+      __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(st + Cfg::KQ + kDeltaBlob);
+      for (int r = n; r < L; ++r)  // rows behind the sequence: zeros
+        for (int x = lane; x < vcols / 8; x += 32)
+          *reinterpret_cast<uint4*>(v + r * LDV + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+      __syncwarp();
+      const uint32_t kq = OUT ? Cfg::KQ : Cfg::KQ / 2, bl = OUT ? kDeltaBlob : kDeltaBlob - kDeltaMat;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, kq + bl + n * vcols * 2);
+        bulk_load(st, p.kq + (static_cast<long>(slot0 + c) * d.qk_heads + hq) * Cfg::KQ, kq, bar);
+        bulk_load(st + Cfg::KQ, p.blobs + (static_cast<long>(slot0 + c) * d.heads + h) * kDeltaBlob, bl, bar);
+      }
+      __syncwarp();
+      if (vcols > 0)
+        for (int r = lane; r < n; r += 32)
+          bulk_load(v + r * LDV,
+                    static_cast<const __nv_bfloat16*>(d.v) + (sr.begin + static_cast<long>(c) * L + r) * d.ldv +
+                        h * d.d_v + col0,
+                    vcols * 2, bar);
     }
-    __syncwarp();
-    if (vcols > 0)
-      for (int r = lane; r < n; r += 32)
-        bulk_load(v + r * LDV,
-                  static_cast<const __nv_bfloat16*>(d.v) + (sr.begin + static_cast<long>(c) * L + r) * d.ldv + h * d.d_v + col0,
-                  vcols * 2, bar);
-  };
-  if (warp == 0 && c0 < c1) load(c0);
+    return;
+  }
 
   // S^T of this warp's 16 columns (rows g and g + 8 of the accumulators), by 8 rows of the state
   const int g = lane >> 2, q2 = 2 * (lane & 3);
@@ -404,12 +482,8 @@ __global__ void __launch_bounds__(256, 1) delta_chunk_kernel(const DeltaChunkPar
   const int m_row = (lane & 7) + ((lane >> 4) << 3), m_col = ((lane >> 3) & 1) * 8;  // (n, k) blocks of a row-major B
   const int t_row = lane & 15, t_col = (lane >> 4) * 8;                              // (k, n) blocks, transposed
   for (int c = c0; c < c1; ++c) {
-    fence_proxy_async_smem();  // (outputs were staged there)
-    __syncthreads();           // every warp is done with the stage that is loaded next
-    if (warp == 0 && c + 1 < c1) load(c + 1);
-    uint8_t* st = sm + ((c - c0) & 1) * Cfg::STAGE;
+    uint8_t* st = sm + ((c - c0) & 1) * STAGE;
     if (!warp_wait(&full[(c - c0) & 1], ((c - c0) >> 1) & 1, abort_flag, d.status)) break;
-    if (my >= cols) continue;  // (a warp without columns only keeps the block going)
     const uint32_t sK = smem_u32(st), sQ = sK + Cfg::KQ / 2, sT = sK + Cfg::KQ, sP = sT + 2 * kDeltaMat + kDeltaScal;
     const float* scal = reinterpret_cast<const float*>(st + Cfg::KQ + 2 * kDeltaMat);
     const uint32_t sV = sT + kDeltaBlob + 16 * warp * 2;
@@ -589,6 +663,9 @@ __global__ void __launch_bounds__(256, 1) delta_chunk_kernel(const DeltaChunkPar
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t + u][e] = fmaf(D[u][e], w_up[e >> 1], a * S[t + u][e]);
     }
+    fence_proxy_async_smem();  // (outputs were staged where the next loads go)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[(c - c0) & 1]);
   }
 
   float* end = nullptr;
@@ -609,56 +686,92 @@ __global__ void __launch_bounds__(256, 1) delta_chunk_kernel(const DeltaChunkPar
 }
 
 // The state before each part: starts[0] = B_0 + M_0 state_in, starts[s] = B_s +
-// M_s starts[s - 1] (fp32 products). One block for 32 columns of one (sequence,
-// head); 256 threads, 4 x 4 values each (DK = 128), M^T staged in shared memory.
+// M_s starts[s - 1] (fp32). One block for 16 columns of one (sequence, head), a
+// thread for 4 x 4 values; the next part's M is fetched while this one's is used.
 template <int DK>
-__global__ void __launch_bounds__(DK * 2) delta_join_kernel(const DeltaChunkParams p) {
+struct DeltaJoinCfg {
+  static constexpr int LDM = DK + 4;
+  static constexpr int SMEM = (2 * DK * LDM + DK * 16) * 4;
+};
+template <int DK>
+__global__ void __launch_bounds__(DK) delta_join_kernel(const DeltaChunkParams p) {
   pdl_wait();
+  constexpr int LDM = DeltaJoinCfg<DK>::LDM;
   extern __shared__ __align__(128) uint8_t dsm[];
-  uint8_t* sm = dsm;
   const DeltaParams& d = p.d;
-  float* sMt = reinterpret_cast<float*>(sm);  // [DK (k)][DK + 4 (row)]
-  float* sS = sMt + DK * (DK + 4);            // [DK][32]
-  const int h = blockIdx.y, seq = blockIdx.z, col0 = blockIdx.x * 32;
+  float* sM = reinterpret_cast<float*>(dsm);  // [2][DK][LDM]
+  float* sS = sM + 2 * DK * LDM;              // [DK][16]
+  const int h = blockIdx.y, seq = blockIdx.z, col0 = blockIdx.x * 16;
   const long head = static_cast<long>(seq) * d.heads + h;
   const int cols = d.d_v + d.d_k, tid = threadIdx.x;
-  const int r0 = (tid >> 3) * 4, x0 = (tid & 7) * 4;  // this thread's rows and columns
-  for (int e = tid; e < DK * 32; e += DK * 2) {
-    const int i = e >> 5, j = col0 + (e & 31);
-    sS[e] = d.state_in && i < d.d_k && j < d.d_v ? d.state_in[(head * d.d_k + i) * d.d_v + j] : 0.f;
+  const int r0 = (tid >> 2) * 4, x0 = (tid & 3) * 4;  // this thread's rows and columns
+  const bool in = col0 + x0 < d.d_v;
+  auto fetch = [&](int s) {  // M_s; rows and columns past d_k are left as they are: their products meet zeros of S
+    const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols + d.d_v;
+    float* to = sM + (s & 1) * DK * LDM;
+    for (int e = tid; e < d.d_k * (d.d_k / 4); e += DK) {
+      const int i = e / (d.d_k / 4), k = (e % (d.d_k / 4)) * 4;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + i * LDM + k)),
+                   "l"(tr + static_cast<long>(i) * cols + k)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int e = tid; e < 2 * DK * LDM / 4; e += DK) *reinterpret_cast<float4*>(sM + 4 * e) = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  fetch(0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d.state_in && in && r0 + i < d.d_k)
+      a = *reinterpret_cast<const float4*>(d.state_in + (head * d.d_k + r0 + i) * d.d_v + col0 + x0);
+    *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
   }
   for (int s = 0; s + 1 < p.nseg; ++s) {
-    const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols;
-    for (int e = tid; e < DK * DK; e += DK * 2) {
-      const int i = e / DK, k = e % DK;
-      sMt[k * (DK + 4) + i] = i < d.d_k && k < d.d_k ? tr[static_cast<long>(i) * cols + d.d_v + k] : 0.f;
-    }
-    __syncthreads();
+    const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols + col0 + x0;
     float acc[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = r0 + i < d.d_k && col0 + x0 + j < d.d_v ? tr[static_cast<long>(r0 + i) * cols + col0 + x0 + j] : 0.f;
-#pragma unroll 4
-    for (int k = 0; k < DK; ++k) {
-      const float4 m = *reinterpret_cast<const float4*>(sMt + k * (DK + 4) + r0);
-      const float4 v = *reinterpret_cast<const float4*>(sS + k * 32 + x0);
-      const float mi[4] = {m.x, m.y, m.z, m.w}, vj[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(mi[i], vj[j], acc[i][j]);
+    for (int i = 0; i < 4; ++i) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in && r0 + i < d.d_k) a = *reinterpret_cast<const float4*>(tr + static_cast<long>(r0 + i) * cols);
+      acc[i][0] = a.x; acc[i][1] = a.y; acc[i][2] = a.z; acc[i][3] = a.w;
+    }
+    if (s + 2 < p.nseg) {
+      fetch(s + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    float* to = p.starts + (head * (p.nseg - 1) + s) * d.d_k * d.d_v;
+    const float* M = sM + (s & 1) * DK * LDM;
+#pragma unroll 2
+    for (int k = 0; k < DK; k += 4) {
+      float4 m[4], v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sS[(r0 + i) * 32 + x0 + j] = acc[i][j];
-        if (r0 + i < d.d_k && col0 + x0 + j < d.d_v) to[static_cast<long>(r0 + i) * d.d_v + col0 + x0 + j] = acc[i][j];
+      for (int i = 0; i < 4; ++i) {
+        m[i] = *reinterpret_cast<const float4*>(M + (r0 + i) * LDM + k);
+        v[i] = *reinterpret_cast<const float4*>(sS + (k + i) * 16 + x0);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float mk[4] = {m[i].x, m[i].y, m[i].z, m[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i][0] = fmaf(mk[j], v[j].x, acc[i][0]);
+          acc[i][1] = fmaf(mk[j], v[j].y, acc[i][1]);
+          acc[i][2] = fmaf(mk[j], v[j].z, acc[i][2]);
+          acc[i][3] = fmaf(mk[j], v[j].w, acc[i][3]);
+        }
+      }
+    }
+    __syncthreads();
+    float* to = p.starts + (head * (p.nseg - 1) + s) * d.d_k * d.d_v + col0 + x0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
+      if (in && r0 + i < d.d_k) *reinterpret_cast<float4*>(to + static_cast<long>(r0 + i) * d.d_v) = a;
+    }
   }
 }
 

@@ -238,17 +238,18 @@ struct DeltaPlan {
 
 // Parts each sequence's chunks are cut into: with few (sequence, head) pairs the
 // walk over the chunks leaves SMs idle. A part's effect is found first (pass 1,
-// on d_v + d_k columns), joined part after part (about 1.5 chunks' time each),
-// then the parts run side by side (pass 2). The number with the least time, in
-// chunks.
+// on d_v + d_k columns), the effects are joined part after part, then the parts
+// run side by side (pass 2). The number with the least time, in chunks of pass 2
+// (measured: a chunk of pass 1 takes 0.87, a join 1.5; 8192 tokens of 16 heads of
+// 128: 842 us in one part, 448 in 4, 386 in 5, 358 in 9, 406 in 16).
 int delta_nseg(const edit_delta_rule* a, int64_t chunks, int sms) {
   const int64_t heads = static_cast<int64_t>(a->nseq) * a->heads;
   const int64_t b1 = heads * ceil_div(a->d_v + a->d_k, kDeltaCols), b2 = heads * ceil_div(a->d_v, kDeltaCols);
   int best = 1;
   double least = static_cast<double>(ceil_div(b2, sms)) * chunks;
   for (int n = 2; n <= kDeltaMaxSeg; ++n) {
-    const double t = static_cast<double>(ceil_div(b1 * (n - 1), sms) + ceil_div(b2 * n, sms)) * ceil_div(chunks, n) + 1.5 * n;
-    if (t < 0.9 * least) {
+    const double t = (0.87 * ceil_div(b1 * (n - 1), sms) + ceil_div(b2 * n, sms)) * ceil_div(chunks, n) + 1.5 * n;
+    if (t < least) {
       least = t;
       best = n;
     }
@@ -283,15 +284,17 @@ int delta_chunked(const DeltaChunkParams& p, cudaStream_t st) {
   auto blocks = [&](int cols, int parts) {
     return dim3(static_cast<unsigned>(ceil_div(cols, kDeltaCols) * parts * d.nseq), d.heads);
   };
-  auto warps = [](int cols) { return dim3(static_cast<unsigned>(32 * ceil_div(cols < kDeltaCols ? cols : kDeltaCols, 16))); };
+  auto warps = [](int cols) { return static_cast<int>(ceil_div(cols < kDeltaCols ? cols : kDeltaCols, 16)); };
   if (p.nseg > 1) {
     const int cols = d.d_v + d.d_k;
-    EDIT_TRY(launch(delta_chunk_kernel<DK, false>, blocks(cols, p.nseg - 1), warps(cols), DeltaChunkCfg<DK>::SMEM, st, p,
+    EDIT_TRY(launch(delta_chunk_kernel<DK, false>, blocks(cols, p.nseg - 1), dim3(32 * warps(cols) + 32),
+                    DeltaChunkCfg<DK>::smem(warps(cols)), st, p,
                     static_cast<int>(ceil_div(cols, kDeltaCols))));
-    EDIT_TRY(launch(delta_join_kernel<DK>, dim3(static_cast<unsigned>(ceil_div(d.d_v, 32)), d.heads, d.nseq), dim3(DK * 2),
-                    (DK * (DK + 4) + DK * 32) * sizeof(float), st, p));
+    EDIT_TRY(launch(delta_join_kernel<DK>, dim3(static_cast<unsigned>(ceil_div(d.d_v, 16)), d.heads, d.nseq), dim3(DK),
+                    DeltaJoinCfg<DK>::SMEM, st, p));
   }
-  return launch(delta_chunk_kernel<DK, true>, blocks(d.d_v, p.nseg), warps(d.d_v), DeltaChunkCfg<DK>::SMEM, st, p,
+  return launch(delta_chunk_kernel<DK, true>, blocks(d.d_v, p.nseg), dim3(32 * warps(d.d_v) + 32),
+                DeltaChunkCfg<DK>::smem(warps(d.d_v)), st, p,
                 static_cast<int>(ceil_div(d.d_v, kDeltaCols)));
 }
 
