@@ -306,16 +306,35 @@ int norm_launch(const BlockNormParams& p, cudaStream_t st) {
   return launch(block_norm_kernel<T, VEC, TPR, NV>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p);
 }
 
+template <typename T, int VEC, int TPR, int NV>
+int norm_rows(const BlockNormParams& p, cudaStream_t st) {
+  // three blocks an SM where there are rows for them (each folds a sample's vectors once)
+  const long most = 3L * device_sms(), per = ceil_div(p.rows, 256 / TPR) <= most ? 256 / TPR : ceil_div(p.rows, most);
+  return launch(block_norm_rows_kernel<T, VEC, TPR, NV>, dim3(static_cast<unsigned>(ceil_div(p.rows, per))), dim3(256),
+                static_cast<size_t>((p.C + 3) / 4) * 64, st, p, static_cast<int>(per));
+}
+
+// Threads a row: a warp where its registers hold the row (40 values a thread in
+// bf16, 16 in fp32, which fills an SM with warps all the same), else 128 or 256;
+// a block's all for rows without 16-byte vectors or few of them.
 template <typename T>
 int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
-  if (vec) {
-    if (p.C <= 512) return norm_launch<T, 8, 32, 2>(p, st);
-    if (p.C <= 1280) return norm_launch<T, 8, 32, 5>(p, st);
-    if (p.C <= 2048) return norm_launch<T, 8, 32, 8>(p, st);
-    return norm_launch<T, 8, 256, 8>(p, st);
+  if (p.C > kBnNarrow) {
+    if (!vec) return norm_launch<T, 1, 256, 64>(p, st);
+    return p.C <= 4096 ? norm_launch<T, 8, 256, 2>(p, st) : norm_launch<T, 8, 256, 8>(p, st);
   }
-  if (p.C <= 2048) return norm_launch<T, 1, 256, 8>(p, st);
-  return norm_launch<T, 1, 256, 64>(p, st);
+  if (!vec) return p.C <= 512 ? norm_rows<T, 1, 128, 4>(p, st) : norm_rows<T, 1, 256, 8>(p, st);
+  const int nv = p.C / 8;
+  if (p.rows > 2L * device_sms()) {
+    if (nv <= 32) return norm_rows<T, 8, 32, 1>(p, st);
+    if (nv <= 64) return norm_rows<T, 8, 32, 2>(p, st);
+    if (sizeof(T) == 2) {
+      if (nv <= 96) return norm_rows<T, 8, 32, 3>(p, st);
+      if (nv <= 128) return norm_rows<T, 8, 32, 4>(p, st);
+      if (nv <= 160) return norm_rows<T, 8, 32, 5>(p, st);
+    }
+  }
+  return nv <= 128 ? norm_rows<T, 8, 128, 1>(p, st) : norm_rows<T, 8, 128, 2>(p, st);
 }
 
 }  // namespace
