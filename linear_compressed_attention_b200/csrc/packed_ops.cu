@@ -130,8 +130,10 @@ int attn_tc(const PackedAttnParams& p, cudaStream_t st) {
   const cuuint64_t sk[2] = {d * 2, static_cast<cuuint64_t>(p.ldk) * 2}, sv[2] = {d * 2, static_cast<cuuint64_t>(p.ldv) * 2};
   if (!bf16_tensor_map(&mk, 3, p.k, dims, sk, box) || !bf16_tensor_map(&mv, 3, p.v, dims, sv, box))
     return EDIT_ERR_CUDA;
-  return launch(packed_attn_tc_kernel<DP, NQ>, dim3(p.slots, p.kv_heads, p.nsplit), dim3(Cfg::THREADS), Cfg::SMEM, st,
-                mq, mk, mv, p);
+  const long items = static_cast<long>(p.slots) * p.kv_heads * p.nsplit, most = (NQ == 1 ? 2L : 1L) * device_sms();
+  if (items > INT32_MAX - most) return EDIT_ERR_UNSUPPORTED;
+  return launch(packed_attn_tc_kernel<DP, NQ>, dim3(static_cast<unsigned>(items < most ? items : most)),
+                dim3(Cfg::THREADS), Cfg::SMEM, st, mq, mk, mv, p, static_cast<int>(items));
 }
 
 template <int NQ>
