@@ -87,6 +87,28 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // mbar_wait / warp_wait without a function call: ptxas allocates no registers
 // beyond a call in a kernel that moves registers between its warps.
 __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
@@ -128,7 +150,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* odd_values = abort_flag + 1;  // the guard cleared values that are not finite (in any item so far)
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int W_TMA = NQ * 4, W_MMA = W_TMA + 1, W_GUARD = W_TMA + 2;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
@@ -169,7 +191,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     uint32_t guarded = 0;  // bit s: parity of v_ok / v_load of slot s
     if (warp == W_TMA) {
       // ---------------------------------------------------------- producer: Q, then K_0 V_0 K_1 V_1 ...
-      int n = 0, s = 0;            // loads so far, and their slot
+      int s = 0;                     // slot of the next load
       uint32_t empty = 1, qe = ~0u;  // parities to wait for
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         AttnWork<NQ> w;
@@ -196,7 +218,6 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
               tma_load_3d(t & 1 ? &mv : &mk, &kv_full[s], sKV + s * TILE + b * BOX, 64 * b, w.hk,
                           w.it.k0 + w.it.kbeg + (t >> 1) * 128);
             if ((t & 1) && (t >> 1) >= w.clean) mbar_arrive(&v_load[s]);
-            ++n;
             if (++s == SLOTS) {
               s = 0;
               empty ^= 1;
@@ -213,24 +234,26 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     } else if (warp == W_MMA) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t tmem = *tmem_slot;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_wait(bar, parity, abort_flag, p.status); };
+      // the whole warp walks along, one lane issues (see umma_bf16_by)
+      const uint32_t leader = elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_warp_wait(bar, parity, abort_flag, p.status); };
       auto scores = [&](int i, int slot) {  // S_i = Q_i K^T
         const uint64_t qd = sdesc_kmajor_sw128(smem_u32(sQ + i * TILE));
         const uint64_t kd = sdesc_kmajor_sw128(smem_u32(sKV + slot * TILE));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint64_t step = ((k >> 2) * BOX + (k & 3) * 32) >> 4;
-          umma_bf16(tmem + 128 * i, qd + step, kd + step, Cfg::IDESC_S, k > 0 ? 1u : 0u);
+          umma_bf16_by(leader, tmem + 128 * i, qd + step, kd + step, Cfg::IDESC_S, k > 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[i]);
+        umma_commit_by(leader, &s_full[i]);
       };
       auto weigh = [&](int i, int slot, bool first) {  // O_i += P_i V
         const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(sKV + slot * TILE), BOX);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          umma_bf16_ts(tmem + NQ * 128 + DP * i, tmem + 128 * i + 8 * k, vd + (2048 >> 4) * k, Cfg::IDESC_O,
+          umma_bf16_ts_by(leader, tmem + NQ * 128 + DP * i, tmem + 128 * i + 8 * k, vd + (2048 >> 4) * k, Cfg::IDESC_O,
                        (!first || k > 0) ? 1u : 0u);
-        umma_commit(&o_full[i]);
+        umma_commit_by(leader, &o_full[i]);
       };
       int s = 0;          // slot of the next tile to use
       uint32_t full = 0;  // its parity
@@ -244,57 +267,54 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         AttnWork<NQ> w;
         if (!attn_work<NQ>(p, item, w) || w.most == 0) continue;
-        if (lane == 0) {
-          ok = wait(&kv_full[s], full);
+        ok = wait(&kv_full[s], full);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          if (w.tiles[i] == 0 || !ok) continue;
+          ok = wait(&q_full[i], (qf >> i) & 1);
+          if (!ok) break;
+          qf ^= 1u << i;
+          tc_fence_after();
+          scores(i, s);
+          if (w.tiles[i] == 1) umma_commit_by(leader, &q_empty[i]);
+        }
+        if (ok) umma_commit_by(leader, &kv_empty[s]);
+        next(s, full);
+        for (int t = 0; t < w.most && ok; ++t) {
+          const int vs = s;
+          ok = wait(&kv_full[vs], full);
+          if (ok && t >= w.clean) {
+            ok = wait(&v_ok[vs], (guarded >> vs) & 1);
+            guarded ^= 1u << vs;
+          }
+          next(s, full);  // now the next K
+          bool key_waited = false;
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
-            if (w.tiles[i] == 0 || !ok) continue;
-            ok = wait(&q_full[i], (qf >> i) & 1);
+            if (!ok || t >= w.tiles[i]) continue;
+            ok = wait(&p_full[i], (pf >> i) & 1);
             if (!ok) break;
-            qf ^= 1u << i;
+            pf ^= 1u << i;
             tc_fence_after();
-            scores(i, s);
-            if (w.tiles[i] == 1) umma_commit(&q_empty[i]);
-          }
-          if (ok) umma_commit(&kv_empty[s]);
-          next(s, full);
-          for (int t = 0; t < w.most && ok; ++t) {
-            const int vs = s;
-            ok = wait(&kv_full[vs], full);
-            if (ok && t >= w.clean) {
-              ok = wait(&v_ok[vs], (guarded >> vs) & 1);
-              guarded ^= 1u << vs;
-            }
-            next(s, full);  // now the next K
-            bool key_waited = false;
-#pragma unroll
-            for (int i = 0; i < NQ; ++i) {
-              if (!ok || t >= w.tiles[i]) continue;
-              ok = wait(&p_full[i], (pf >> i) & 1);
-              if (!ok) break;
-              pf ^= 1u << i;
-              tc_fence_after();
-              weigh(i, vs, t == 0);
-              if (t + 1 < w.tiles[i]) {
-                if (!key_waited) {
-                  ok = wait(&kv_full[s], full);
-                  if (!ok) break;
-                  key_waited = true;
-                  tc_fence_after();
-                }
-                scores(i, s);
-                if (t + 2 == w.tiles[i]) umma_commit(&q_empty[i]);  // the item's last reads of its Q
+            weigh(i, vs, t == 0);
+            if (t + 1 < w.tiles[i]) {
+              if (!key_waited) {
+                ok = wait(&kv_full[s], full);
+                if (!ok) break;
+                key_waited = true;
+                tc_fence_after();
               }
+              scores(i, s);
+              if (t + 2 == w.tiles[i]) umma_commit_by(leader, &q_empty[i]);  // the item's last reads of its Q
             }
-            if (!ok) break;
-            umma_commit(&kv_empty[vs]);
-            if (t + 1 < w.most) {
-              umma_commit(&kv_empty[s]);
-              next(s, full);
-            }
+          }
+          if (!ok) break;
+          umma_commit_by(leader, &kv_empty[vs]);
+          if (t + 1 < w.most) {
+            umma_commit_by(leader, &kv_empty[s]);
+            next(s, full);
           }
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
     } else {
       // ---------------------------------------------------------- V guard, two warps
@@ -398,9 +418,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             for (int x = 0; x < 64; x += 8)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mx[k] = fmaxf(mx[k], fmaxf(s[HOLD ? half : 0][x + k], s[HOLD ? half : 0][x + 4 + k]));
+                mx[k] = max3(mx[k], s[HOLD ? half : 0][x + 2 * k], s[HOLD ? half : 0][x + 2 * k + 1]);
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
           const bool grow = top > m + 8.f || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? top : m;
@@ -425,7 +445,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             m = mn;
           }
           const float base = m == -INFINITY ? 0.f : m;
-          float sum[4] = {};
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
 #pragma unroll
           for (int x0 = 0; x0 < 128; x0 += 32) {
             if (!HOLD && (x0 & 63) == 0) fetch(x0 >> 6);  // (P lies over columns of S already read)
@@ -434,15 +455,16 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
               const int y = (x0 & 63) + x;
-              const float a = ex2_approx(fmaf(v[y], c, -base)), b = ex2_approx(fmaf(v[y + 1], c, -base));
-              sum[x & 2] += a;
-              sum[(x & 2) + 1] += b;
-              u[x >> 1] = pack_bf16x2(a, b);
+              float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], e);
+              u[x >> 1] = pack_bf16x2(e.x, e.y);
             }
             tmem_st16(tS + x0 / 2, u);
           }
           tmem_st_wait();
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         tc_fence_before();
         __syncwarp();
