@@ -36,7 +36,8 @@ struct AttnTcCfg {
   static constexpr int TILE = NBX * BOX;            // one Q, K or V tile
   static constexpr int SLOTS = NQ == 1 ? (DP == 64 ? 4 : 2) : (DP == 64 ? 8 : 5);  // ring of K and V tiles
   static constexpr int BARS = NQ * 5 + 4 * SLOTS;
-  static constexpr int SMEM = 1024 + (NQ + SLOTS) * TILE + BARS * 8 + 16;
+  static constexpr int BATCH = 24;                  // items whose work is found at a time
+  static constexpr int SMEM = 1024 + (NQ + SLOTS) * TILE + BARS * 8 + 16 + BATCH * 64;
   static_assert(SMEM * (NQ == 1 ? 2 : 1) + (NQ == 1 ? 2048 : 0) <= 232448 + 1024, "shared memory");
   // two row tiles: launched with 168 registers a thread, 200 for the softmax warps and 104 for the others (256 x 200 +
   // 128 x 104 = 384 x 168)
@@ -47,35 +48,61 @@ struct AttnTcCfg {
 };
 
 // One item of a block's work: row tile(s) of a slot, a key/value head and a part
-// of the keys. All 32 lanes call; false for an empty slot.
+// of the keys.
 template <int NQ>
 struct AttnWork {
-  AttnItem it;
+  int q_row, ntok;  // first row of q, tokens (0: an empty slot)
+  int k_row;        // row of k of the first key, kbeg
+  int kbeg, kend;   // key range within the sequence (kend: what the item's last row sees)
+  int see0;         // keys that the item's first row sees (below 1: none)
   int hk, split;
-  int tiles[NQ];  // key tiles of each row tile
-  int most;       // the most of them
-  int all_see;    // keys that every row sees: 0 .. all_see - 1; V tiles reaching beyond have masked keys
-  int clean;      // key tiles before the first of those
+  int tiles[NQ];    // key tiles of each row tile
+  int most;         // the most of them
+  int clean;        // key tiles all of whose keys every row sees; V tiles from there on have masked keys
 };
 template <int NQ>
-__device__ __forceinline__ bool attn_work(const PackedAttnParams& p, int item, AttnWork<NQ>& w) {
-  const int R = 128 / (p.heads / p.kv_heads);  // tokens a row tile
-  w.split = item % p.nsplit;
-  w.hk = (item / p.nsplit) % p.kv_heads;
-  // last slots first: in a causal sequence they see the most keys
-  if (!attn_item<128>(p, p.slots - 1 - item / (p.nsplit * p.kv_heads), w.split, NQ * R, w.it)) return false;
-  w.most = 0;
+__device__ __forceinline__ void attn_work(const PackedAttnParams& p, int item, int G, AttnWork<NQ>& w) {
+  const int R = 128 / G;  // tokens a row tile
+  w.split = 0;
+  if (p.nsplit > 1) {
+    w.split = item % p.nsplit;
+    item /= p.nsplit;
+  }
+  const int slot = p.slots - 1 - item / p.kv_heads;  // last slots first: in a causal sequence they see the most keys
+  w.hk = item % p.kv_heads;
+  // the slot's sequence: the last one whose first slot is at or before it (see seq_of_slot)
+  int s = 0;
+  for (int n = p.nseq; n > 1;) {
+    const int half = n / 2, first = clamp_int(p.q_offsets[s + half], 0, p.rows_q) / (NQ * R) + s + half;
+    s += first <= slot ? half : 0;
+    n = first <= slot ? n - half : half;
+  }
+  const SeqRows q = seq_rows(p.q_offsets, s, p.rows_q), k = seq_keys(p, s);
+  const int tile = slot - (q.begin / (NQ * R) + s);
+  w.ntok = tile < 0 || tile > (q.len - 1) / (NQ * R) || q.len == 0 ? 0 : min(NQ * R, q.len - tile * NQ * R);
+  w.most = w.clean = 0;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) w.tiles[i] = 0;
+  if (w.ntok == 0) return;
+  const int tok0 = tile * NQ * R, shift = k.len - q.len;
+  w.q_row = q.begin + tok0;
+  w.kbeg = 0;
+  w.kend = p.causal ? clamp_int(tok0 + w.ntok + shift, 0, k.len) : k.len;
+  w.see0 = p.causal ? tok0 + 1 + shift : k.len;
+  if (p.nsplit > 1) {  // whole tiles but the last
+    const long nt = (w.kend + 127) / 128;
+    w.kbeg = static_cast<int>(nt * w.split / p.nsplit) * 128;
+    w.kend = min(w.kend, static_cast<int>(nt * (w.split + 1) / p.nsplit) * 128);
+  }
+  w.k_row = k.begin + w.kbeg;
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {  // those that the tile's last row sees (within this part)
-    const int n = min(w.it.ntok - i * R, R);  // tokens
-    int kend = w.it.kend;
-    if (p.causal) kend = min(kend, w.it.tok0 + i * R + n + w.it.lk - w.it.lq);
-    w.tiles[i] = n > 0 && kend > w.it.kbeg ? (kend - w.it.kbeg + 127) / 128 : 0;
+    const int n = min(w.ntok - i * R, R);  // tokens
+    const int kend = p.causal ? min(w.kend, tok0 + i * R + n + shift) : w.kend;
+    w.tiles[i] = n > 0 && kend > w.kbeg ? (kend - w.kbeg + 127) / 128 : 0;
     w.most = max(w.most, w.tiles[i]);
   }
-  w.all_see = min(w.it.kend, p.causal ? clamp_int(w.it.tok0 + 1 + w.it.lk - w.it.lq, 0, w.it.lk) : w.it.lk);
-  w.clean = max(0, min(w.most, (w.all_see - w.it.kbeg) / 128));
-  return true;
+  w.clean = max(0, min(w.most, (min(w.kend, w.see0) - w.kbeg) / 128));
 }
 
 template <int R>
@@ -150,6 +177,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* odd_values = abort_flag + 1;  // the guard cleared values that are not finite (in any item so far)
 
+  AttnWork<NQ>* work = reinterpret_cast<AttnWork<NQ>*>(tmem_slot + 4);  // [BATCH]
+  static_assert(sizeof(AttnWork<NQ>) <= 64, "work");
+
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int W_TMA = NQ * 4, W_MMA = W_TMA + 1, W_GUARD = W_TMA + 2;
   if (threadIdx.x == 0) {
@@ -184,7 +214,17 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
   tc_fence_after();
 
   // Each role walks the block's items by itself, so that the loads and the first scores of an item run under the
-  // end of the one before (a block for every item cost 10 us each, launch, setup and drain).
+  // end of the one before. What the items are is found for a batch of them at once, one thread each (found by every
+  // role for every item it took 8 us an item, a chain of loads and divisions).
+  const int G = p.heads / p.kv_heads, R = 128 / G;
+  auto batch = [&](int first) {  // all threads of the block; returns the items of the batch
+    named_bar_sync(1, Cfg::THREADS);  // the last batch is done with
+    const int item = first + static_cast<int>(threadIdx.x * gridDim.x);
+    if (threadIdx.x < Cfg::BATCH && item < items) attn_work<NQ>(p, item, G, work[threadIdx.x]);
+    named_bar_sync(1, Cfg::THREADS);
+    return min(+Cfg::BATCH, (items - first + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  };
+  const int stride = Cfg::BATCH * static_cast<int>(gridDim.x);
   if (warp >= W_TMA) {
     if constexpr (NQ == 2) regs_dec<104>();
     bool ok = true;
@@ -193,11 +233,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
       // ---------------------------------------------------------- producer: Q, then K_0 V_0 K_1 V_1 ...
       int s = 0;                     // slot of the next load
       uint32_t empty = 1, qe = ~0u;  // parities to wait for
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        AttnWork<NQ> w;
-        if (!attn_work<NQ>(p, item, w)) continue;
-        const int G = p.heads / p.kv_heads, R = 128 / G;
-        if (lane == 0) {
+      for (int first = blockIdx.x; first < items; first += stride)
+        for (int left = batch(first), e = 0; e < left; ++e) {
+        const AttnWork<NQ> w = work[e];
+        if (lane == 0 && ok) {
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
             if (w.tiles[i] == 0 || !ok) continue;
@@ -207,7 +246,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             mbar_arrive_expect_tx(&q_full[i], NBX * R * G * 128);
 #pragma unroll
             for (int b = 0; b < NBX; ++b)
-              tma_load_4d(&mq, &q_full[i], sQ + i * TILE + b * BOX, 64 * b, 0, w.hk, w.it.q0 + w.it.tok0 + i * R);
+              tma_load_4d(&mq, &q_full[i], sQ + i * TILE + b * BOX, 64 * b, 0, w.hk, w.q_row + i * R);
           }
           for (int t = 0; t < 2 * w.most && ok; ++t) {
             ok = attn_wait(&kv_empty[s], empty, abort_flag, p.status);
@@ -216,7 +255,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
 #pragma unroll
             for (int b = 0; b < NBX; ++b)
               tma_load_3d(t & 1 ? &mv : &mk, &kv_full[s], sKV + s * TILE + b * BOX, 64 * b, w.hk,
-                          w.it.k0 + w.it.kbeg + (t >> 1) * 128);
+                          w.k_row + (t >> 1) * 128);
             if ((t & 1) && (t >> 1) >= w.clean) mbar_arrive(&v_load[s]);
             if (++s == SLOTS) {
               s = 0;
@@ -264,9 +303,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
           par ^= 1;
         }
       };
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        AttnWork<NQ> w;
-        if (!attn_work<NQ>(p, item, w) || w.most == 0) continue;
+      for (int first = blockIdx.x; first < items; first += stride)
+        for (int left = batch(first), e = 0; e < left; ++e) {
+        const AttnWork<NQ> w = work[e];
+        if (w.most == 0 || !ok) continue;
         ok = wait(&kv_full[s], full);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
@@ -319,13 +359,13 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     } else {
       // ---------------------------------------------------------- V guard, two warps
       int n = 0;  // tiles loaded before this item
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        AttnWork<NQ> w;
-        if (!attn_work<NQ>(p, item, w)) continue;
+      for (int first = blockIdx.x; first < items; first += stride)
+        for (int left = batch(first), e = 0; e < left && ok; ++e) {
+        const AttnWork<NQ> w = work[e];
         const int n0 = n;
         n += 2 * w.most;
         for (int t = w.clean; t < w.most; ++t) {
-          const int nv = n0 + 2 * t + 1, s = nv % SLOTS, key0 = w.it.kbeg + t * 128;
+          const int nv = n0 + 2 * t + 1, s = nv % SLOTS, key0 = w.kbeg + t * 128;
           // (the load's issue first: before it, kv_full's parity could be that of a use two back)
           if (!attn_warp_wait(&v_load[s], (guarded >> s) & 1, abort_flag, p.status) ||
               !attn_warp_wait(&kv_full[s], (nv / SLOTS) & 1, abort_flag, p.status)) {
@@ -334,8 +374,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
           }
           guarded ^= 1u << s;
           uint8_t* v = sKV + s * TILE;
-          const int nk = min(128, w.it.kend - key0);            // rows behind are cleared
-          const int from = clamp_int(w.all_see - key0, 0, nk);  // rows before are seen by all
+          const int nk = min(128, w.kend - key0);               // rows behind are cleared
+          const int from = clamp_int(w.see0 - key0, 0, nk);     // rows before are seen by all
           // a warp takes 4 of every 8 rows, 16 bytes a lane
           const int r0 = 4 * (warp - W_GUARD) + (lane >> 3);
           uint8_t* mine = v + (lane & 7) * 16;
@@ -375,19 +415,18 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     const int q4 = warp & 3, r = q4 * 32 + lane;
     const uint32_t t_lane = *tmem_slot + (static_cast<uint32_t>(q4 * 32) << 16);
     const uint32_t tS = t_lane + 128 * i, tO = t_lane + NQ * 128 + DP * i;
-    const int G = p.heads / p.kv_heads, R = 128 / G;
     const float c = p.scale * 1.4426950408889634f;
     uint32_t n_par = 0;  // parity of this row tile's next key tile
     bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      AttnWork<NQ> w;
-      if (!attn_work<NQ>(p, item, w)) continue;
-      const int T = w.tiles[i], kbeg = w.it.kbeg;
-      const int tok = w.it.tok0 + i * R + r / G;  // of the sequence
-      const bool real = r < R * G && tok < w.it.lq;
+    const int r_tok = i * R + r / G, r_head = r % G;  // this row's token of an item and head of a group
+    for (int first = blockIdx.x; first < items; first += stride)
+      for (int left = batch(first), e = 0; e < left; ++e) {
+      const AttnWork<NQ>& w = work[e];
+      if (w.ntok == 0 || !ok) continue;
+      const int T = w.tiles[i], kbeg = w.kbeg;
+      const bool real = r < R * G && r_tok < w.ntok;
       const bool any = __any_sync(0xffffffffu, real);  // a warp without rows only keeps the barriers going
-      int see = w.it.kend;
-      if (p.causal) see = min(see, tok + 1 + w.it.lk - w.it.lq);
+      const int see = p.causal ? min(w.kend, w.see0 + r_tok) : w.kend;  // keys this row sees
       float m = -INFINITY, l = 0.f;  // maximum (of c S) that O and l refer to
       for (int t = 0; t < T; ++t, n_par ^= 1) {
         if (!attn_warp_wait(&s_full[i], n_par, abort_flag, p.status)) {
@@ -471,11 +510,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
         if (lane == 0) mbar_arrive(&p_full[i]);
       }
       if (ok && T > 0) ok = attn_warp_wait(&o_full[i], n_par ^ 1, abort_flag, p.status);
-      if (!ok) break;
-      if (!any) continue;
+      if (!ok || !any) continue;
       tc_fence_after();
-      const long row = w.it.q0 + static_cast<long>(tok);
-      const int h = w.hk * G + r % G;
+      const long row = w.q_row + static_cast<long>(r_tok);
+      const int h = w.hk * G + r_head;
       const long at = (w.split * static_cast<long>(p.rows_q) + row) * p.heads + h;
       const float inv = p.nsplit > 1 ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
       const bool odd = *odd_values;
@@ -490,9 +528,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
           for (int k = 0; k < 16; ++k) o[k] = 0.f;
         }
         if (odd && real) {  // values the guard cleared, for the rows that see them
-          for (int j = max(w.all_see, kbeg + w.clean * 128); j < see; ++j) {
+          for (int j = max(w.see0, kbeg + w.clean * 128); j < see; ++j) {
             const __nv_bfloat16* vj = static_cast<const __nv_bfloat16*>(p.v) +
-                                      (w.it.k0 + static_cast<long>(j)) * p.ldv + w.hk * p.d + x;
+                                      (w.k_row - kbeg + static_cast<long>(j)) * p.ldv + w.hk * p.d + x;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               if (x + k >= p.d) continue;

@@ -131,7 +131,7 @@ int attn_tc(const PackedAttnParams& p, cudaStream_t st) {
   if (!bf16_tensor_map(&mk, 3, p.k, dims, sk, box) || !bf16_tensor_map(&mv, 3, p.v, dims, sv, box))
     return EDIT_ERR_CUDA;
   const long items = static_cast<long>(p.slots) * p.kv_heads * p.nsplit, most = (NQ == 1 ? 2L : 1L) * device_sms();
-  if (items > INT32_MAX - most) return EDIT_ERR_UNSUPPORTED;
+  if (items > INT32_MAX - 64 * most) return EDIT_ERR_UNSUPPORTED;  // (a block's steps stay in 32 bits)
   return launch(packed_attn_tc_kernel<DP, NQ>, dim3(static_cast<unsigned>(items < most ? items : most)),
                 dim3(Cfg::THREADS), Cfg::SMEM, st, mq, mk, mv, p, static_cast<int>(items));
 }
