@@ -579,6 +579,26 @@ typedef struct {
 EDIT_API int edit_block_norm_forward(const void *x, const void *y, const edit_block_norm *a, void *r, void *h,
                                      void *stream);
 
+/* The DiT block of edit_dit_block_forward with other norms, and norms after its
+ * branches as well (a block with norms on both sides of each branch), its
+ * residual steps run by the block norm above:
+ *   x1 = x + gate_a * N_post(EDiT(N_pre(x) (1 + scale_a) + shift_a) o_w^T + o_b)
+ *   x2 = x1 + N_post(softmax-attention(..) co_w^T + co_b)
+ *   out = x2 + gate_f * N_post(GELU(N_pre(x2) (1 + scale_f) + shift_f) ..)
+ * norm_pre, norm_post: EDIT_NORM_* (eps: the block's ln_eps), each followed by
+ * its optional weight [C] (NULL: 1; a post weight needs a post norm).
+ * EDIT_NORM_LAYER before and EDIT_NORM_NONE after, without weights, is the
+ * block of edit_dit_block_forward. The rest, workspace included, as there. */
+typedef struct {
+  int norm_pre, norm_post;
+  const void *pre_attn_w, *pre_ffn_w;
+  const void *post_attn_w, *post_cross_w, *post_ffn_w;
+} edit_dit_block_norms;
+
+EDIT_API int edit_dit_block_normed_forward(const void *x, const void *y, const void *t6, int B, int H, int W, int N_T,
+                                           int C, int heads, const edit_dit_block_weights *w,
+                                           const edit_dit_block_norms *norms, void *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,7 @@ EXPORTS = ("edit_attn_workspace_bytes", "edit_attn_forward", "mmedit_workspace_b
            "edit_attn_band_partials", "edit_attn_band_finish", "edit_dit_block_workspace_bytes",
            "edit_dit_block_forward", "edit_packed_attention_workspace_bytes", "edit_packed_attention_forward",
            "edit_delta_rule_workspace_bytes", "edit_delta_rule_forward", "edit_delta_rule_step",
-           "edit_block_norm_forward")
+           "edit_block_norm_forward", "edit_dit_block_normed_forward")
 STAGE_EVENTS_EDIT, STAGE_EVENTS_MM = 9, 12
 PROC = {"none": 0, "cf": 1, "sc": 2}
 VARIANT_NAMES = ("kcf3_w", "kcf3_b", "kgn_gamma", "kgn_beta", "kcf1_w", "kcf1_b", "o_w", "o_b")
@@ -61,6 +61,14 @@ class DitBlockWeights(ctypes.Structure):
     _fields_ = [("attn", EditAttnWeights)] + [(n, ctypes.c_void_p) for n in DIT_NAMES] + \
                [("hidden", ctypes.c_int), ("ln_eps", ctypes.c_float), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)] + _SIDE_FIELDS
+
+
+DIT_NORM_WEIGHTS = ("pre_attn_w", "pre_ffn_w", "post_attn_w", "post_cross_w", "post_ffn_w")
+
+
+class DitBlockNorms(ctypes.Structure):
+    _fields_ = [("norm_pre", ctypes.c_int), ("norm_post", ctypes.c_int)] + \
+               [(n, ctypes.c_void_p) for n in DIT_NORM_WEIGHTS]
 
 
 class EditAttnVariant(ctypes.Structure):
@@ -141,6 +149,8 @@ def lib():
     L.edit_dit_block_workspace_bytes.restype = sz
     L.edit_dit_block_forward.argtypes = [p, p, p, i, i, i, i, i, i, DW, p, p]
     L.edit_dit_block_forward.restype = i
+    L.edit_dit_block_normed_forward.argtypes = [p, p, p, i, i, i, i, i, i, DW, ctypes.POINTER(DitBlockNorms), p, p]
+    L.edit_dit_block_normed_forward.restype = i
     V = ctypes.POINTER(EditAttnVariant)
     L.edit_attn_variant_workspace_bytes.argtypes = [i, i, i, i, i, W, V]
     L.edit_attn_variant_workspace_bytes.restype = sz
@@ -449,13 +459,23 @@ def edit_dit_block_forward(x, y, t6, B, H, W, N_T, C, heads, weights: DitBlockWe
                                             ctypes.byref(weights), _ptr(out), _stream(stream)))
 
 
+def edit_dit_block_normed_forward(x, y, t6, B, H, W, N_T, C, heads, weights: DitBlockWeights, norms: DitBlockNorms,
+                                  out, stream=None) -> int:
+    return int(lib().edit_dit_block_normed_forward(_ptr(x), _ptr(y), _ptr(t6), B, H, W, N_T, C, heads,
+                                                   ctypes.byref(weights), ctypes.byref(norms), _ptr(out),
+                                                   _stream(stream)))
+
+
 class DitBlock:
     """One DiT block (EDiT self-attention, cross-attention over the caption
     tokens, MLP) with weights and workspace on a CUDA device; ``arrays`` is
-    the synthetic-input dict drawn with ``dit_block=...``."""
+    the synthetic-input dict drawn with ``dit_block=...``. ``norms`` = (pre,
+    post[, weights]) names other norms before and after the branches ('none',
+    'layer', 'rms') and a dict of their optional weights (pre_attn_w,
+    pre_ffn_w, post_attn_w, post_cross_w, post_ffn_w: [C] arrays)."""
 
     def __init__(self, arrays: dict, B: int, H: int, W: int, N_T: int, C: int, heads: int, dtype: str = "bf16",
-                 device="cuda", side: bool = True):
+                 device="cuda", side: bool = True, norms: tuple | None = None):
         import torch
         self.torch = torch
         self.B, self.H, self.W, self.N_T, self.C, self.heads = B, H, W, N_T, C, heads
@@ -481,12 +501,23 @@ class DitBlock:
         self.struct = s
         self.side = make_side(device) if side and code == EDIT_BF16 else None
         set_side(self.struct, self.side)
+        self.norms = None
+        if norms is not None:
+            self.norms = DitBlockNorms()
+            self.norms.norm_pre, self.norms.norm_post = NORM[norms[0]], NORM[norms[1]]
+            for n, a in (norms[2] if len(norms) > 2 else {}).items():
+                self.w[n] = torch.from_numpy(np.ascontiguousarray(a)).to(device=device, dtype=self.tdtype)
+                setattr(self.norms, n, self.w[n].data_ptr())
 
     def forward(self, x, y, t6, out=None, stream=None):
         if out is None:
             out = self.torch.empty_like(x)
-        rc = edit_dit_block_forward(x, y, t6, self.B, self.H, self.W, self.N_T, self.C, self.heads, self.struct, out,
-                                    stream)
+        if self.norms is not None:
+            rc = edit_dit_block_normed_forward(x, y, t6, self.B, self.H, self.W, self.N_T, self.C, self.heads,
+                                               self.struct, self.norms, out, stream)
+        else:
+            rc = edit_dit_block_forward(x, y, t6, self.B, self.H, self.W, self.N_T, self.C, self.heads, self.struct,
+                                        out, stream)
         if rc != 0:
             raise EditError(rc)
         return out

@@ -1834,15 +1834,53 @@ int linear_any(const Plan& pl, const void* a, long rows, int K, const void* w, c
   return simt_linear(a, rows, K, ws1, bs1, 1, n, out, static_cast<int>(ldo), act, st);
 }
 
+// One residual step of the block: r = base + g N_post(delta), h = N_pre(r) (1 + scale) + shift, the vectors rows kg,
+// ks, kh of sst + t6 (kg < 0: g = 1). Without `norms` the block's own kernel (LayerNorm before, none after).
+template <typename T>
+int dit_residual(const Plan& pl, const edit_dit_block_weights* w, const edit_dit_block_norms* norms,
+                 const void* post_w, const void* pre_w, const void* base, const void* delta, const void* t6, int kg,
+                 int ks, int kh, void* r_out, void* h_out, cudaStream_t st) {
+  if (!norms)
+    return dit_residual_ln<T>(pl, base, delta, w->sst, t6, kg, ks, kh, w->ln_eps, r_out, h_out, st);
+  edit_block_norm a = {};
+  a.dtype = pl.bf16 ? EDIT_BF16 : EDIT_F32;
+  a.norm_post = delta ? norms->norm_post : EDIT_NORM_NONE;
+  a.norm_pre = h_out ? norms->norm_pre : EDIT_NORM_NONE;
+  a.C = pl.C;
+  a.samples = pl.B;
+  a.eps = w->ln_eps;
+  a.res_scale = 1.f;
+  a.rows = static_cast<int64_t>(pl.B) * pl.HW;
+  a.rows_per_sample = pl.HW;
+  a.ldx = a.ldy = a.ldr = a.ldh = pl.C;
+  a.ld_mod = 6L * pl.C;
+  a.post_w = delta ? post_w : nullptr;
+  a.pre_w = h_out ? pre_w : nullptr;
+  const T *sst = static_cast<const T*>(w->sst), *mod = static_cast<const T*>(t6);
+  auto row = [&](const T* p, int k) { return p + static_cast<long>(k) * pl.C; };
+  if (delta && kg >= 0) {
+    a.gate0 = row(sst, kg);
+    a.gate = row(mod, kg);
+  }
+  if (h_out) {
+    a.scale0 = row(sst, ks);
+    a.scale = row(mod, ks);
+    a.shift0 = row(sst, kh);
+    a.shift = row(mod, kh);
+  }
+  return edit_block_norm_forward(base, delta, &a, r_out, h_out, st);
+}
+
 template <typename T>
 int run_dit(const void* x, const void* y, const void* t6, const DitPlan& dp, const edit_dit_block_weights* w,
-            uint8_t* ws, void* out, cudaStream_t st) {
+            const edit_dit_block_norms* nm, uint8_t* ws, void* out, cudaStream_t st) {
   const Plan& pa = dp.pa;
   const int C = pa.C;
   const long tok = static_cast<long>(pa.B) * pa.HW, trow = static_cast<long>(pa.B) * dp.NT;
   int* status = reinterpret_cast<int*>(ws + pa.status);
   // h1 = LN(x) (1 + scale_a) + shift_a
-  EDIT_TRY(dit_residual_ln<T>(pa, x, nullptr, w->sst, t6, -1, 1, 0, w->ln_eps, nullptr, ws + dp.h1, st));
+  EDIT_TRY(dit_residual<T>(pa, w, nm, nullptr, nm ? nm->pre_attn_w : nullptr, x, nullptr, t6, -1, 1, 0, nullptr,
+                           ws + dp.h1, st));
   // a = EDiT(h1) o_w^T + o_b (resets the status block)
   edit_attn_weights aw = w->attn;
   aw.workspace = ws;
@@ -1850,7 +1888,8 @@ int run_dit(const void* x, const void* y, const void* t6, const DitPlan& dp, con
   const edit_attn_variant var = dit_attn_variant(w);
   EDIT_TRY(run_edit<T>(ws + dp.h1, pa, &aw, ws, ws + dp.att, st, side_of(w->side_stream, w->side_events), &var));
   // x1 = x + gate_a a
-  EDIT_TRY(dit_residual_ln<T>(pa, x, ws + dp.att, w->sst, t6, 2, 0, 0, w->ln_eps, ws + dp.x1, nullptr, st));
+  EDIT_TRY(dit_residual<T>(pa, w, nm, nm ? nm->post_attn_w : nullptr, nullptr, x, ws + dp.att, t6, 2, 0, 0, ws + dp.x1,
+                           nullptr, st));
   // cross-attention over the caption tokens
   EDIT_TRY(linear_any<T>(pa, ws + dp.x1, tok, C, w->cq_w, w->cq_b, C, ws + dp.q, C, ACT_NONE, status, st));
   {
@@ -1891,12 +1930,14 @@ int run_dit(const void* x, const void* y, const void* t6, const DitPlan& dp, con
   }
   EDIT_TRY(linear_any<T>(pa, ws + dp.att, tok, C, w->co_w, w->co_b, C, ws + dp.c, C, ACT_NONE, status, st));
   // x2 = x1 + c; h2 = LN(x2) (1 + scale_f) + shift_f
-  EDIT_TRY(dit_residual_ln<T>(pa, ws + dp.x1, ws + dp.c, w->sst, t6, -1, 4, 3, w->ln_eps, ws + dp.x2, ws + dp.h2, st));
+  EDIT_TRY(dit_residual<T>(pa, w, nm, nm ? nm->post_cross_w : nullptr, nm ? nm->pre_ffn_w : nullptr, ws + dp.x1,
+                           ws + dp.c, t6, -1, 4, 3, ws + dp.x2, ws + dp.h2, st));
   // MLP: f = GELU(h2 fc1^T + b1), m = f fc2^T + b2; out = x2 + gate_f m
   EDIT_TRY(linear_any<T>(pa, ws + dp.h2, tok, C, w->fc1_w, w->fc1_b, dp.hidden, ws + dp.f, dp.hidden, ACT_GELU,
                          status, st));
   EDIT_TRY(linear_any<T>(pa, ws + dp.f, tok, dp.hidden, w->fc2_w, w->fc2_b, C, ws + dp.m, C, ACT_NONE, status, st));
-  return dit_residual_ln<T>(pa, ws + dp.x2, ws + dp.m, w->sst, t6, 5, 0, 0, w->ln_eps, out, nullptr, st);
+  return dit_residual<T>(pa, w, nm, nm ? nm->post_ffn_w : nullptr, nullptr, ws + dp.x2, ws + dp.m, t6, 5, 0, 0, out,
+                         nullptr, st);
 }
 
 int dit_checks(const void* x, const void* y, const void* t6, const void* out, const edit_dit_block_weights* w,
@@ -2062,8 +2103,30 @@ int edit_dit_block_forward(const void* x, const void* y, const void* t6, int B, 
   EDIT_TRY(dit_checks(x, y, t6, out, w, dp));
   uint8_t* ws = static_cast<uint8_t*>(w->workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dp.pa.bf16 ? run_dit<__nv_bfloat16>(x, y, t6, dp, w, ws, out, st)
-                    : run_dit<float>(x, y, t6, dp, w, ws, out, st);
+  return dp.pa.bf16 ? run_dit<__nv_bfloat16>(x, y, t6, dp, w, nullptr, ws, out, st)
+                    : run_dit<float>(x, y, t6, dp, w, nullptr, ws, out, st);
+}
+
+int edit_dit_block_normed_forward(const void* x, const void* y, const void* t6, int B, int H, int W, int N_T, int C,
+                                  int heads, const edit_dit_block_weights* w, const edit_dit_block_norms* norms,
+                                  void* out, void* stream) {
+  DitPlan dp;
+  if (!norms) return EDIT_ERR_NULL;
+  EDIT_TRY(make_dit_plan(B, H, W, N_T, C, heads, w, dp));
+  EDIT_TRY(dit_checks(x, y, t6, out, w, dp));
+  // what edit_block_norm_forward would refuse in the middle of the call
+  for (int kind : {norms->norm_pre, norms->norm_post})
+    if (kind < EDIT_NORM_NONE || kind > EDIT_NORM_RMS) return EDIT_ERR_UNSUPPORTED;
+  const void* weights[] = {norms->pre_attn_w, norms->pre_ffn_w, norms->post_attn_w, norms->post_cross_w,
+                           norms->post_ffn_w};
+  for (int i = 0; i < 5; ++i) {
+    if (!aligned(weights[i], 16)) return EDIT_ERR_ALIGN;
+    if (weights[i] && (i < 2 ? norms->norm_pre : norms->norm_post) == EDIT_NORM_NONE) return EDIT_ERR_UNSUPPORTED;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(w->workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dp.pa.bf16 ? run_dit<__nv_bfloat16>(x, y, t6, dp, w, norms, ws, out, st)
+                    : run_dit<float>(x, y, t6, dp, w, norms, ws, out, st);
 }
 
 const char* edit_status_string(int status) {

@@ -90,9 +90,12 @@ int attn_args(const edit_packed_attention* a) {
 }
 
 // Parts of the key lists when there are `slots` row tiles for each key/value
-// head: enough blocks for every SM, at least 256 keys a part.
+// head: about 12 items an SM, at least 256 keys a part, so that blocks end
+// together whatever the lengths (one token of 32 sequences over caches of up to
+// 8192 keys, 8 heads: 143 us with 1 part, 125 with 4, 120 with 6, 127 with 9, 143
+// with 18, where the parts' own start and the join weigh more).
 int attn_nsplit(long slots, const edit_packed_attention* a, int sms) {
-  const long want = sms / (slots * a->kv_heads), most = ceil_div(a->max_k, 256);
+  const long want = 12L * sms / (slots * a->kv_heads), most = ceil_div(a->max_k, 256);
   const long n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n);
 }

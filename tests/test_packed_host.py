@@ -142,3 +142,31 @@ def test_block_norm_refuses(kw, code):
 def test_block_norm_null_struct_and_no_rows():
     assert bd.lib().edit_block_norm_forward(P(1), P(1), None, P(1), P(1), None) == NULL
     assert norm_call(rows=0) == 0     # nothing is enqueued
+
+
+def test_dit_block_norms_refused():
+    L, n = bd.lib(), bd.DitBlockNorms()
+    w = bd.DitBlockWeights()
+    s = bd.EditAttnWeights()
+    s.dtype, s.c_red, s.gn_groups = 1, 288, 32
+    for k, name in enumerate(bd.WEIGHT_NAMES):
+        setattr(s, name, 0x10000 + 0x1000 * k)       # never dereferenced: validation fails first
+    w.attn, w.hidden, w.ln_eps = s, 512, 1e-6
+    for k, name in enumerate(bd.DIT_NAMES):
+        setattr(w, name, 0x80000 + 0x1000 * k)
+    w.workspace, w.workspace_bytes = 0x1000000, 1 << 40
+
+    def call(norms=n, x=0x2000000):
+        return L.edit_dit_block_normed_forward(P(x), P(0x3000000), P(0x4000000), 1, 64, 64, 300, 1152, 16,
+                                               ctypes.byref(w), None if norms is None else ctypes.byref(norms),
+                                               P(0x5000000), None)
+    assert call(norms=None) == NULL
+    assert call(x=0) == NULL
+    n.norm_pre = 3
+    assert call() == UNSUPPORTED
+    n.norm_pre, n.norm_post = 1, -1
+    assert call() == UNSUPPORTED
+    n.norm_post, n.post_cross_w = 0, 0x6000000       # a post weight without a post norm
+    assert call() == UNSUPPORTED
+    n.norm_post, n.post_cross_w = 2, 0x6000008
+    assert call() == ALIGN
