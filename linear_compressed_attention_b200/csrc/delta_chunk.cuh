@@ -22,8 +22,9 @@
 // and split into two fp16 halves (22 bits), k (8 bits) is exact in fp16 after
 // such a scaling, and T is split as well; the dropped product of two low halves
 // is 2^-22. (Two bf16 halves would leave 2^-17 and three would cost half as many
-// products again.) O is rounded to bf16, so its products take one half: fp16 for
-// Q^ S0, bf16 for P U, whose terms a decay may set many powers of two apart.
+// products again.) O is rounded to bf16, so Q^ S0 takes one fp16 half, and P U,
+// whose terms a decay may set many powers of two apart, P in bf16 and U in two
+// bf16 halves (with U in one, O was 1.5 times as far off as its own rounding).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -583,11 +584,13 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
       float Op[8][4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t a[4];
+        uint32_t a[4], lo[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int t = 2 * k + (b >> 1), r = b & 1;
           a[b] = pack_bf16x2(U[t][2 * r], U[t][2 * r + 1]);
+          lo[b] = pack_bf16x2(U[t][2 * r] - __uint_as_float(a[b] << 16),
+                              U[t][2 * r + 1] - __uint_as_float(a[b] & 0xffff0000u));
         }
 #pragma unroll
         for (int t = k; t < 4; ++t) {
@@ -595,6 +598,8 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
           ldsm_x4(sP + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
           mma_bf16(Op[2 * t], a, b[0], b[1]);
           mma_bf16(Op[2 * t + 1], a, b[2], b[3]);
+          mma_bf16(Op[2 * t], lo, b[0], b[1]);
+          mma_bf16(Op[2 * t + 1], lo, b[2], b[3]);
         }
       }
 #pragma unroll
