@@ -39,150 +39,283 @@ __device__ __forceinline__ void load4(const T* p, float* o) {
   }
 }
 
-// Token by token, the state in registers. A warp holds 16 columns of one
-// (sequence, head)'s state: lane = 8 cg + l keeps columns 4 cg .. 4 cg + 3 and
-// the rows 4 (l + 8 m) .. + 3, so that a state row's 16 columns are 64
-// contiguous bytes and the sums over d_k are three shuffles over 8 lanes. Both
+// Token by token, the state in registers. A warp holds 4 CPT columns of one
+// (sequence, head)'s state: lane = 8 cg + l keeps columns CPT cg .. and the rows
+// 4 (l + 8 m) .. + 3, so that the sums over d_k are three shuffles over 8 lanes.
+// CPT is 4 for single tokens (a state row's 16 columns are 64 contiguous bytes;
+// they are bound by the state's bytes) and 2 for sequences, where a warp's
+// instructions per token are the time (4: 0.37 us a token, d_k = 64). Both
 // products with the state, S^T k and S^T q, are taken of the state before the
 // token (o = e^g S^T q + (k.q) u), so that a token costs one round of shuffles.
 // The state is kept as S / A with A the decay since it was last brought up to
 // date (every 16 tokens, or when the log of A leaves +-8): a rounding of every
 // value for the decay of every token was most of the state's error (400 fp32
 // tokens: 1.1e-6 of its norm).
-template <typename T, int DK>
+// STEP: one token of each sequence, straight from memory. Otherwise the block's
+// tokens come 16 at a time through shared memory, copied while the 16 before
+// them are worked on, and what does not depend on the state (norms, k.q, the
+// decays) is found for the 16 at once before the walk (in the walk it was half
+// of a token's 0.4 us, which is all latency).
+constexpr int kDeltaTokens = 16;
+
+template <bool STEP>
+constexpr int kDeltaCpt = STEP ? 4 : 2;  // columns a thread; 16 times that a block
+
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float* o) {
+  if constexpr (N == 4) {
+    load4(p, o);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    o[0] = __uint_as_float(u << 16);
+    o[1] = __uint_as_float(u & 0xffff0000u);
+  } else {
+    const float2 a = *reinterpret_cast<const float2*>(p);
+    o[0] = a.x; o[1] = a.y;
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* p, const float* o) {
+  if constexpr (sizeof(T) == 2 && N == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  else if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(o[0], o[1]);
+  else if constexpr (N == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+  else
+    *reinterpret_cast<float2*>(p) = make_float2(o[0], o[1]);
+}
+
+template <typename T, int DK, int COLS>
+struct DeltaTokens {  // one stage
+  T q[kDeltaTokens][DK], k[kDeltaTokens][DK], v[kDeltaTokens][COLS];
+  float g[kDeltaTokens], beta[kDeltaTokens];
+};
+
+struct DeltaScalars {
+  float rk, rq;    // 1 / |k| (or 1), scale / |q|
+  float kq;        // k . q
+  float settle;    // the factor that brings the state up to date before the token, 1 for none
+  float A, invA;   // decay held back after it, and its inverse
+};
+
+// The decay of the next token joins what is held back; past +-8, or with `all`, everything is settled (a NaN settles).
+__device__ __forceinline__ void hold_decay(float& logA, float g, bool all, DeltaScalars& x) {
+  logA += log_decay(g);
+  x.settle = x.A = x.invA = 1.f;
+  if (all || !(fabsf(logA) <= 8.f)) {
+    x.settle = expf(logA);
+    logA = 0.f;
+  }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <typename T, int DK, bool STEP>
 __global__ void __launch_bounds__(128) delta_recurrent_kernel(const DeltaParams p, int col_blocks) {
   pdl_wait();
   if (p.status && blockIdx.x == 0 && blockIdx.y == 0)
     check_offsets(p.offsets, p.rows, nullptr, 0, nullptr, 0, p.nseq, p.status);
-  constexpr int RM = DK / 32;
-  const int s = blockIdx.x / col_blocks, h = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
-  const int c0 = (((blockIdx.x % col_blocks) * 4 + warp) * 4 + (lane >> 3)) * 4;
-  if (((blockIdx.x % col_blocks) * 4 + warp) * 16 >= p.d_v) return;  // whole warps
+  constexpr int RM = DK / 32, CPT = kDeltaCpt<STEP>, COLS = 16 * CPT;
+  using Tokens = DeltaTokens<T, DK, COLS>;
+  __shared__ __align__(16) Tokens stage[STEP ? 1 : 2];
+  __shared__ DeltaScalars scal[kDeltaTokens];
+  const int s = blockIdx.x / col_blocks, h = blockIdx.y, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31, l = lane & 7;
+  const int b0 = (blockIdx.x % col_blocks) * COLS, x0 = (warp * 4 + (lane >> 3)) * CPT, c0 = b0 + x0;
   const bool live = c0 < p.d_v;
-  const SeqRows sr = p.offsets ? seq_rows(p.offsets, s, static_cast<int>(p.rows)) : SeqRows{s, 1};
+  const SeqRows sr = STEP ? SeqRows{s, 1} : seq_rows(p.offsets, s, static_cast<int>(p.rows));
   const int hq = h / (p.heads / p.qk_heads);
   const long st_at = (static_cast<long>(s) * p.heads + h) * p.d_k * p.d_v + c0;
-  float S[RM][4][4];
+  const T* qp = static_cast<const T*>(p.q) + sr.begin * p.ldq + hq * p.d_k;
+  const T* kp = static_cast<const T*>(p.k) + sr.begin * p.ldk + hq * p.d_k;
+  const T* vp = static_cast<const T*>(p.v) + sr.begin * p.ldv + h * p.d_v;
+  const float* gp = p.g + sr.begin * p.ldg + h;
+  const float* bp = p.beta + sr.begin * p.ldb + h;
+  T* op = static_cast<T*>(p.out) + sr.begin * p.ldo + h * p.d_v + c0;
+  auto copy = [&](int t0) {  // tokens t0 .. into their stage
+    Tokens& to = stage[STEP ? 0 : (t0 / kDeltaTokens) & 1];
+    constexpr int V = 16 / sizeof(T);
+    const int n = min(kDeltaTokens, sr.len - t0), ck = p.d_k / V, cv = min(+COLS, p.d_v - b0) / V;
+    for (int e = tid; e < n * ck; e += 128) {
+      const int r = e / ck, x = (e % ck) * V;
+      cp_async<16>(&to.q[r][x], qp + (t0 + r) * p.ldq + x);
+      cp_async<16>(&to.k[r][x], kp + (t0 + r) * p.ldk + x);
+    }
+    for (int e = tid; e < n * cv; e += 128) {
+      const int r = e / cv, x = (e % cv) * V;
+      cp_async<16>(&to.v[r][x], vp + (t0 + r) * p.ldv + b0 + x);
+    }
+    if (tid < n) {
+      cp_async<4>(&to.g[tid], gp + (t0 + tid) * p.ldg);
+      cp_async<4>(&to.beta[tid], bp + (t0 + tid) * p.ldb);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (!STEP) {
+    if (DK > p.d_k)  // columns past d_k stay zero
+      for (int e = tid; e < 2 * kDeltaTokens * DK; e += 128) {
+        Tokens& to = stage[e / (kDeltaTokens * DK)];
+        (&to.q[0][0])[e % (kDeltaTokens * DK)] = (&to.k[0][0])[e % (kDeltaTokens * DK)] = from_f32<T>(0.f);
+      }
+    __syncthreads();
+    if (sr.len > 0) copy(0);
+  }
+  float S[RM][4][CPT] = {};
 #pragma unroll
   for (int m = 0; m < RM; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * (l + 8 * m) + i;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.state_in && live && r < p.d_k)
-        a = *reinterpret_cast<const float4*>(p.state_in + st_at + static_cast<long>(r) * p.d_v);
-      S[m][i][0] = a.x; S[m][i][1] = a.y; S[m][i][2] = a.z; S[m][i][3] = a.w;
+      if (p.state_in && live && r < p.d_k) load_n<float, CPT>(p.state_in + st_at + static_cast<long>(r) * p.d_v, S[m][i]);
     }
-  const T* qp = static_cast<const T*>(p.q) + sr.begin * p.ldq + hq * p.d_k + 4 * l;
-  const T* kp = static_cast<const T*>(p.k) + sr.begin * p.ldk + hq * p.d_k + 4 * l;
-  const T* vp = static_cast<const T*>(p.v) + sr.begin * p.ldv + h * p.d_v + c0;
-  const float* gp = p.g + sr.begin * p.ldg + h;
-  const float* bp = p.beta + sr.begin * p.ldb + h;
-  T* op = static_cast<T*>(p.out) + sr.begin * p.ldo + h * p.d_v + c0;
-  float qn[RM][4], kn[RM][4], vn[4], gn = 0.f, bn = 0.f;
-  auto fetch = [&](long t) {  // token t into the registers of the next step
-#pragma unroll
-    for (int m = 0; m < RM; ++m) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qn[m][i] = kn[m][i] = 0.f;
-      if (4 * (l + 8 * m) < p.d_k) {
-        load4(qp + t * p.ldq + 32 * m, qn[m]);
-        load4(kp + t * p.ldk + 32 * m, kn[m]);
-      }
-    }
-    vn[0] = vn[1] = vn[2] = vn[3] = 0.f;
-    if (live) load4(vp + t * p.ldv, vn);
-    gn = gp[t * p.ldg];
-    bn = bp[t * p.ldb];
-  };
-  float logA = 0.f, A = 1.f, invA = 1.f;
-  int held = 0;
+  float logA = 0.f;  // (of the thread that finds the decays)
+  float A = 1.f;
   auto settle = [&](float f) {
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[m][i][j] *= f;
-    logA = 0.f;
-    A = invA = 1.f;
-    held = 0;
+        for (int j = 0; j < CPT; ++j) S[m][i][j] *= f;
   };
-  if (sr.len > 0) fetch(0);
-  for (int t = 0; t < sr.len; ++t) {
-    float q[RM][4], k[RM][4], v[4];
+  auto sum8 = [](float v) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  auto norms = [&](float kk, float qq, float kq, DeltaScalars& x) {
+    x.rk = p.qk_norm ? rsqrtf(kk + p.qk_eps) : 1.f;
+    x.rq = p.scale * (p.qk_norm ? rsqrtf(qq + p.qk_eps) : 1.f);
+    x.kq = kq;
+  };
+  auto token = [&](long t, const float (&q)[RM][4], const float (&k)[RM][4], const float (&v)[CPT], float beta,
+                   const DeltaScalars& x) {
+    if (x.settle != 1.f) settle(x.settle);
+    A = x.A;
+    float red[2 * CPT] = {};  // S^T k, S^T q
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[m][i] = qn[m][i];
-        k[m][i] = kn[m][i];
-      }
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = vn[j];
-    const float beta = bn;
-    logA += log_decay(gn);
-    if (!(fabsf(logA) <= 8.f) || ++held == 16) {  // (a NaN settles, and stays)
-      settle(expf(logA));
-    } else {
-      A = expf(logA);
-      invA = expf(-logA);
-    }
-    if (t + 1 < sr.len) fetch(t + 1);
-    float red[11] = {};  // S^T k (4 columns), S^T q (4), |k|^2, |q|^2, k.q
-#pragma unroll
-    for (int m = 0; m < RM; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < CPT; ++j) {
           red[j] = fmaf(S[m][i][j], k[m][i], red[j]);
-          red[4 + j] = fmaf(S[m][i][j], q[m][i], red[4 + j]);
+          red[CPT + j] = fmaf(S[m][i][j], q[m][i], red[CPT + j]);
         }
-        red[8] = fmaf(k[m][i], k[m][i], red[8]);
-        red[9] = fmaf(q[m][i], q[m][i], red[9]);
-        red[10] = fmaf(k[m][i], q[m][i], red[10]);
-      }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < 11; ++i) red[i] += __shfl_xor_sync(0xffffffffu, red[i], o);
-    float rk = 1.f, rq = p.scale;
-    if (p.qk_norm) {
-      rk = rsqrtf(red[8] + p.qk_eps);
-      rq *= rsqrtf(red[9] + p.qk_eps);
-    }
-    float u[4], o4[4];
+      for (int i = 0; i < 2 * CPT; ++i) red[i] += __shfl_xor_sync(0xffffffffu, red[i], o);
+    float u[CPT], o[CPT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u[j] = beta * (v[j] - A * rk * red[j]) * rk;  // (times 1/|k|: the state adds k u)
-      o4[j] = rq * fmaf(red[10], u[j], A * red[4 + j]);
-      u[j] *= invA;
+    for (int j = 0; j < CPT; ++j) {
+      u[j] = beta * (v[j] - A * x.rk * red[j]) * x.rk;  // (times 1/|k|: the state adds k u)
+      o[j] = x.rq * fmaf(x.kq, u[j], A * red[CPT + j]);
+      u[j] *= x.invA;
     }
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[m][i][j] = fmaf(k[m][i], u[j], S[m][i][j]);
-    if (l == 0 && live) {
-      if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint2*>(op + t * p.ldo) = make_uint2(pack_bf16x2(o4[0], o4[1]), pack_bf16x2(o4[2], o4[3]));
-      else
-        *reinterpret_cast<float4*>(op + t * p.ldo) = make_float4(o4[0], o4[1], o4[2], o4[3]);
+        for (int j = 0; j < CPT; ++j) S[m][i][j] = fmaf(k[m][i], u[j], S[m][i][j]);
+    if (l == 0 && live) store_n<T, CPT>(op + t * p.ldo, o);
+  };
+  if constexpr (STEP) {
+    float q[RM][4], k[RM][4], v[CPT] = {};
+#pragma unroll
+    for (int m = 0; m < RM; ++m) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[m][i] = k[m][i] = 0.f;
+      if (4 * (l + 8 * m) < p.d_k) {
+        load4(qp + 4 * l + 32 * m, q[m]);
+        load4(kp + 4 * l + 32 * m, k[m]);
+      }
+    }
+    if (live) load_n<T, CPT>(vp + c0, v);
+    float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+    for (int m = 0; m < RM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kk = fmaf(k[m][i], k[m][i], kk);
+        qq = fmaf(q[m][i], q[m][i], qq);
+        kq = fmaf(k[m][i], q[m][i], kq);
+      }
+    DeltaScalars x;
+    norms(sum8(kk), sum8(qq), sum8(kq), x);
+    hold_decay(logA, gp[0], true, x);
+    token(0, q, k, v, bp[0], x);
+  } else {
+    for (int t0 = 0; t0 < sr.len; t0 += kDeltaTokens) {
+      if (t0 + kDeltaTokens < sr.len) {
+        copy(t0 + kDeltaTokens);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      __syncthreads();
+      const Tokens& in = stage[STEP ? 0 : (t0 / kDeltaTokens) & 1];
+      const int n = min(kDeltaTokens, sr.len - t0);
+      {  // 8 threads a token
+        const int r = tid >> 3;
+        float kk = 0.f, qq = 0.f, kq = 0.f;
+        if (r < n)
+          for (int x = 4 * (tid & 7); x < DK; x += 32) {
+            float q[4], k[4];
+            load4(&in.q[r][x], q);
+            load4(&in.k[r][x], k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              kk = fmaf(k[i], k[i], kk);
+              qq = fmaf(q[i], q[i], qq);
+              kq = fmaf(k[i], q[i], kq);
+            }
+          }
+        kk = sum8(kk);
+        qq = sum8(qq);
+        kq = sum8(kq);
+        if (r < n && (tid & 7) == 0) norms(kk, qq, kq, scal[r]);
+        if (tid == 127)  // what is held back never passes the 16 tokens
+          for (int i = 0; i < n; ++i) {
+            hold_decay(logA, in.g[i], i == n - 1, scal[i]);
+            scal[i].A = logA;
+          }
+        __syncthreads();
+        if (tid < n) {
+          const float a = scal[tid].A;
+          scal[tid].A = expf(a);
+          scal[tid].invA = expf(-a);
+        }
+        __syncthreads();
+      }
+      for (int r = 0; r < n; ++r) {
+        float q[RM][4], k[RM][4], v[CPT];
+#pragma unroll
+        for (int m = 0; m < RM; ++m) {
+          load4(&in.q[r][4 * l + 32 * m], q[m]);
+          load4(&in.k[r][4 * l + 32 * m], k[m]);
+        }
+        load_n<T, CPT>(&in.v[r][x0], v);  // (of columns that are not there: whatever it is, they are never stored)
+        token(t0 + r, q, k, v, in.beta[r], scal[r]);
+      }
+      __syncthreads();  // the stage is copied over next
     }
   }
-  settle(A);
   if (p.state_out && live) {
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * (l + 8 * m) + i;
-        if (r < p.d_k)
-          *reinterpret_cast<float4*>(p.state_out + st_at + static_cast<long>(r) * p.d_v) =
-              make_float4(S[m][i][0], S[m][i][1], S[m][i][2], S[m][i][3]);
+        if (r < p.d_k) store_n<float, CPT>(p.state_out + st_at + static_cast<long>(r) * p.d_v, S[m][i]);
       }
   }
 }

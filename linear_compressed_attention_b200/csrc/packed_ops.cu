@@ -176,7 +176,7 @@ int delta_args(const edit_delta_rule* a, bool step) {
   if (a->d_k % 8 != 0 || a->d_k > 128 || a->d_v % 8 != 0 || a->d_v > 256 || a->heads > 65535)
     return EDIT_ERR_UNSUPPORTED;
   if (!step && a->rows > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
-  if (static_cast<long>(a->nseq) * 4 * kDeltaMaxSeg > INT32_MAX || (!step && a->nseq > 65535)) return EDIT_ERR_UNSUPPORTED;
+  if (static_cast<long>(a->nseq) * 8 * kDeltaMaxSeg > INT32_MAX || (!step && a->nseq > 65535)) return EDIT_ERR_UNSUPPORTED;
   return EDIT_OK;
 }
 
@@ -221,14 +221,14 @@ DeltaParams delta_params(const void* q, const void* k, const void* v, const floa
   return p;
 }
 
-template <typename T>
+template <typename T, bool STEP>
 int delta_recurrent(const DeltaParams& p, cudaStream_t st) {
-  const int cb = static_cast<int>(ceil_div(p.d_v, 64));
+  const int cb = static_cast<int>(ceil_div(p.d_v, 16 * kDeltaCpt<STEP>));
   const dim3 grid(static_cast<unsigned>(p.nseq) * cb, p.heads), block(128);
-  if (p.d_k <= 32) return launch(delta_recurrent_kernel<T, 32>, grid, block, 0, st, p, cb);
-  if (p.d_k <= 64) return launch(delta_recurrent_kernel<T, 64>, grid, block, 0, st, p, cb);
-  if (p.d_k <= 96) return launch(delta_recurrent_kernel<T, 96>, grid, block, 0, st, p, cb);
-  return launch(delta_recurrent_kernel<T, 128>, grid, block, 0, st, p, cb);
+  if (p.d_k <= 32) return launch(delta_recurrent_kernel<T, 32, STEP>, grid, block, 0, st, p, cb);
+  if (p.d_k <= 64) return launch(delta_recurrent_kernel<T, 64, STEP>, grid, block, 0, st, p, cb);
+  if (p.d_k <= 96) return launch(delta_recurrent_kernel<T, 96, STEP>, grid, block, 0, st, p, cb);
+  return launch(delta_recurrent_kernel<T, 128, STEP>, grid, block, 0, st, p, cb);
 }
 
 // bf16 calls with sequences of at least this many rows on average run in chunks
@@ -460,7 +460,7 @@ int edit_delta_rule_forward(const void* q, const void* k, const void* v, const f
     c.starts = reinterpret_cast<float*>(ws + pl.starts);
     return pl.DK == 64 ? delta_chunked<64>(c, st) : delta_chunked<128>(c, st);
   }
-  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16>(p, st) : delta_recurrent<float>(p, st);
+  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16, false>(p, st) : delta_recurrent<float, false>(p, st);
 }
 
 int edit_delta_rule_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -474,7 +474,7 @@ int edit_delta_rule_step(const void* q, const void* k, const void* v, const floa
   p.state_in = state;
   p.state_out = state;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16>(p, st) : delta_recurrent<float>(p, st);
+  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16, true>(p, st) : delta_recurrent<float, true>(p, st);
 }
 
 int edit_block_norm_forward(const void* x, const void* y, const edit_block_norm* a, void* r, void* h, void* stream) {
