@@ -320,4 +320,92 @@ __global__ void __launch_bounds__(128) delta_recurrent_kernel(const DeltaParams 
   }
 }
 
+// One token of each of many sequences: a block brings a whole (sequence, head)
+// state in with one bulk copy (it is contiguous), keeps its values in registers
+// between the two passes over them and sends it back the same way. A thread has
+// one column and every RS-th row. Bound by the state's bytes, read and written:
+// what matters is how many are under way, three blocks of 64 KB an SM here against
+// 128 KB in the registers of delta_recurrent_kernel (64 sequences x 32 heads of
+// 128 x 128: 55 us against 72).
+template <typename T, int DV>
+__global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
+  pdl_wait();
+  constexpr int RS = 256 / DV, RPT = 128 / RS;  // row groups; rows a thread at most
+  extern __shared__ __align__(128) uint8_t dsm[];
+  float* sS = reinterpret_cast<float*>(dsm);  // [d_k][DV]
+  __shared__ float sk[128], sq[128], part[8][3], red[RS][2][DV];
+  __shared__ __align__(8) uint64_t full;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = tid % DV, rg = tid / DV;
+  const int h = blockIdx.y, s = blockIdx.x, hq = h / (p.heads / p.qk_heads);
+  const uint32_t bytes = static_cast<uint32_t>(p.d_k) * DV * 4;
+  float* state = p.state_out + (static_cast<long>(s) * p.heads + h) * p.d_k * DV;
+  if (tid == 0) {
+    abort_flag = 0;
+    mbar_init(&full, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&full, bytes);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(sS)),
+                 "l"(state), "r"(bytes), "r"(smem_u32(&full))
+                 : "memory");
+  }
+  float k = 0.f, q = 0.f;
+  if (tid < p.d_k) {
+    k = to_f32(static_cast<const T*>(p.k)[s * p.ldk + hq * p.d_k + tid]);
+    q = to_f32(static_cast<const T*>(p.q)[s * p.ldq + hq * p.d_k + tid]);
+  }
+  const float v = to_f32(static_cast<const T*>(p.v)[s * p.ldv + h * DV + c]);
+  const float a = expf(log_decay(p.g[s * p.ldg + h])), beta = p.beta[s * p.ldb + h];
+  if (tid < 128) {
+    sk[tid] = k;
+    sq[tid] = q;
+    const float kk = warp_sum(k * k), qq = warp_sum(q * q), kq = warp_sum(k * q);
+    if (lane == 0) {
+      part[warp][0] = kk;
+      part[warp][1] = qq;
+      part[warp][2] = kq;
+    }
+  }
+  __syncthreads();
+  float n[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) n[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+  const float rk = p.qk_norm ? rsqrtf(n[0] + p.qk_eps) : 1.f;
+  const float rq = p.scale * (p.qk_norm ? rsqrtf(n[1] + p.qk_eps) : 1.f);
+  const bool ok = mbar_wait(&full, 0, &abort_flag, nullptr);
+  float S[RPT], r1 = 0.f, r2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = rg + RS * i;
+    S[i] = r < p.d_k ? a * sS[r * DV + c] : 0.f;
+    r1 = fmaf(S[i], sk[r], r1);
+    r2 = fmaf(S[i], sq[r], r2);
+  }
+  red[rg][0][c] = r1;
+  red[rg][1][c] = r2;
+  __syncthreads();
+  r1 = r2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < RS; ++i) {
+    r1 += red[i][0][c];
+    r2 += red[i][1][c];
+  }
+  const float u = beta * (v - rk * r1) * rk;  // (times 1/|k|: the state adds k u)
+  if (rg == 0 && ok) static_cast<T*>(p.out)[s * p.ldo + h * DV + c] = from_f32<T>(rq * fmaf(n[2], u, r2));
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = rg + RS * i;
+    if (r < p.d_k) sS[r * DV + c] = fmaf(sk[r], u, S[i]);
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0 && ok) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(state), "r"(smem_u32(sS)), "r"(bytes)
+                 : "memory");
+    bulk_commit();
+    bulk_wait_all();
+  }
+}
+
 }  // namespace edit

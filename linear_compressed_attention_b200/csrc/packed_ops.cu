@@ -231,6 +231,20 @@ int delta_recurrent(const DeltaParams& p, cudaStream_t st) {
   return launch(delta_recurrent_kernel<T, 128, STEP>, grid, block, 0, st, p, cb);
 }
 
+// Single tokens: whole states through shared memory where two blocks for every SM
+// are there to bring them in, else smaller blocks.
+template <typename T>
+int delta_single(const DeltaParams& p, cudaStream_t st) {
+  const long blocks = static_cast<long>(p.nseq) * p.heads;
+  const size_t bytes = static_cast<size_t>(p.d_k) * p.d_v * 4;
+  if (blocks >= 2L * device_sms()) {
+    const dim3 grid(static_cast<unsigned>(p.nseq), p.heads), block(256);
+    if (p.d_v == 128) return launch(delta_step_kernel<T, 128>, grid, block, bytes, st, p);
+    if (p.d_v == 64) return launch(delta_step_kernel<T, 64>, grid, block, bytes, st, p);
+  }
+  return delta_recurrent<T, true>(p, st);
+}
+
 // bf16 calls with sequences of at least this many rows on average run in chunks
 // of 64 tokens, others token by token.
 constexpr int kDeltaChunkedRows = 32;
@@ -474,7 +488,7 @@ int edit_delta_rule_step(const void* q, const void* k, const void* v, const floa
   p.state_in = state;
   p.state_out = state;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a->dtype == EDIT_BF16 ? delta_recurrent<__nv_bfloat16, true>(p, st) : delta_recurrent<float, true>(p, st);
+  return a->dtype == EDIT_BF16 ? delta_single<__nv_bfloat16>(p, st) : delta_single<float>(p, st);
 }
 
 int edit_block_norm_forward(const void* x, const void* y, const edit_block_norm* a, void* r, void* h, void* stream) {

@@ -88,6 +88,26 @@ def test_step_is_one_token(dtype, hq, h, dk, dv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,h,dk,dv", [(16, 16, 128, 128), (8, 16, 72, 64), (16, 32, 8, 128), (16, 16, 40, 72)])
+def test_step_of_many_sequences(dtype, hq, h, dk, dv):
+    # enough states for the kernel that takes whole states (d_v 64 and 128); strided inputs
+    S = 24
+    q, k, v, g, beta = inputs(17, dtype, S, hq, h, dk, dv)
+    g[3] = -float("inf")
+    state = torch.randn(S, h, dk, dv, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    op = bd.DeltaRule(hq, h, dk, dv, S, 0, dtype, scale=0.7)
+    ref = R.delta_rule(q, k, v, g, beta, list(range(S + 1)), state, 0.7, True)
+    qk = torch.cat([q, k], 1)
+    wide = torch.full((S, h + 1, dv), 3.0, device="cuda", dtype=v.dtype)
+    for _ in range(2):
+        mine = state.clone()
+        op.step(qk[:, :hq], qk[:, hq:], v, g, beta, mine, out=wide[:, :h])
+        assert (wide[:, h] == 3.0).all()
+        check(wide[:, :h], mine, ref, [0, S])
+    assert torch.equal(mine, (lambda m: (op.step(q, k, v, g, beta, m), m)[1])(state.clone()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_then_single_tokens_is_the_whole_sequence(dtype):
     hq, h, dk, dv = 2, 4, 64, 64
     lens = [100, 3]
