@@ -126,7 +126,7 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool real
 }
 
 template <int DK>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaChunkParams p) {
+__global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkParams p) {
   pdl_wait();
   const DeltaParams& d = p.d;
   if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -691,30 +691,33 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
 }
 
 // The state before each part: starts[0] = B_0 + M_0 state_in, starts[s] = B_s +
-// M_s starts[s - 1] (fp32). One block for 16 columns of one (sequence, head), a
-// thread for 4 x 4 values; the next part's M is fetched while this one's is used.
+// M_s starts[s - 1] (fp32). One block for 16 columns of one (sequence, head); a
+// thread sums half of the products of 4 x 4 values (the steps are dependent, so
+// their latency is the time: 5.3 us a step with whole sums, 128 x 128); the next
+// part's M is fetched while this one's is used.
 template <int DK>
 struct DeltaJoinCfg {
   static constexpr int LDM = DK + 4;
-  static constexpr int SMEM = (2 * DK * LDM + DK * 16) * 4;
+  static constexpr int SMEM = (2 * DK * LDM + 2 * DK * 16) * 4;
 };
 template <int DK>
-__global__ void __launch_bounds__(DK) delta_join_kernel(const DeltaChunkParams p) {
+__global__ void __launch_bounds__(2 * DK) delta_join_kernel(const DeltaChunkParams p) {
   pdl_wait();
   constexpr int LDM = DeltaJoinCfg<DK>::LDM;
   extern __shared__ __align__(128) uint8_t dsm[];
   const DeltaParams& d = p.d;
   float* sM = reinterpret_cast<float*>(dsm);  // [2][DK][LDM]
   float* sS = sM + 2 * DK * LDM;              // [DK][16]
+  float* sH = sS + DK * 16;                   // [DK][16] sums of the second half
   const int h = blockIdx.y, seq = blockIdx.z, col0 = blockIdx.x * 16;
   const long head = static_cast<long>(seq) * d.heads + h;
   const int cols = d.d_v + d.d_k, tid = threadIdx.x;
-  const int r0 = (tid >> 2) * 4, x0 = (tid & 3) * 4;  // this thread's rows and columns
-  const bool in = col0 + x0 < d.d_v;
+  const int half = tid / DK, r0 = ((tid % DK) >> 2) * 4, x0 = (tid & 3) * 4;  // this thread's half, rows and columns
+  const bool in = half == 0 && col0 + x0 < d.d_v;
   auto fetch = [&](int s) {  // M_s; rows and columns past d_k are left as they are: their products meet zeros of S
     const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols + d.d_v;
     float* to = sM + (s & 1) * DK * LDM;
-    for (int e = tid; e < d.d_k * (d.d_k / 4); e += DK) {
+    for (int e = tid; e < d.d_k * (d.d_k / 4); e += 2 * DK) {
       const int i = e / (d.d_k / 4), k = (e % (d.d_k / 4)) * 4;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + i * LDM + k)),
                    "l"(tr + static_cast<long>(i) * cols + k)
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(DK) delta_join_kernel(const DeltaChunkParams p
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  for (int e = tid; e < 2 * DK * LDM / 4; e += DK) *reinterpret_cast<float4*>(sM + 4 * e) = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = tid; e < 2 * DK * LDM / 4; e += 2 * DK) *reinterpret_cast<float4*>(sM + 4 * e) = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
   fetch(0);
 #pragma unroll
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(DK) delta_join_kernel(const DeltaChunkParams p
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (d.state_in && in && r0 + i < d.d_k)
       a = *reinterpret_cast<const float4*>(d.state_in + (head * d.d_k + r0 + i) * d.d_v + col0 + x0);
-    *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
+    if (half == 0) *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
   }
   for (int s = 0; s + 1 < p.nseg; ++s) {
     const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols + col0 + x0;
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(DK) delta_join_kernel(const DeltaChunkParams p
     __syncthreads();
     const float* M = sM + (s & 1) * DK * LDM;
 #pragma unroll 2
-    for (int k = 0; k < DK; k += 4) {
+    for (int k = half * (DK / 2); k < (half + 1) * (DK / 2); k += 4) {
       float4 m[4], v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -769,13 +772,21 @@ __global__ void __launch_bounds__(DK) delta_join_kernel(const DeltaChunkParams p
         }
       }
     }
+    if (half == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(sH + (r0 + i) * 16 + x0) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    }
     __syncthreads();
     float* to = p.starts + (head * (p.nseg - 1) + s) * d.d_k * d.d_v + col0 + x0;
+    if (half == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 a = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
-      if (in && r0 + i < d.d_k) *reinterpret_cast<float4*>(to + static_cast<long>(r0 + i) * d.d_v) = a;
+      for (int i = 0; i < 4; ++i) {
+        const float4 b = *reinterpret_cast<const float4*>(sH + (r0 + i) * 16 + x0);
+        const float4 a = make_float4(acc[i][0] + b.x, acc[i][1] + b.y, acc[i][2] + b.z, acc[i][3] + b.w);
+        *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
+        if (in && r0 + i < d.d_k) *reinterpret_cast<float4*>(to + static_cast<long>(r0 + i) * d.d_v) = a;
+      }
     }
   }
 }

@@ -309,7 +309,7 @@ int delta_chunked(const DeltaChunkParams& p, cudaStream_t st) {
     EDIT_TRY(launch(delta_chunk_kernel<DK, false>, blocks(cols, p.nseg - 1), dim3(32 * warps(cols) + 32),
                     DeltaChunkCfg<DK>::smem(warps(cols)), st, p,
                     static_cast<int>(ceil_div(cols, kDeltaCols))));
-    EDIT_TRY(launch(delta_join_kernel<DK>, dim3(static_cast<unsigned>(ceil_div(d.d_v, 16)), d.heads, d.nseq), dim3(DK),
+    EDIT_TRY(launch(delta_join_kernel<DK>, dim3(static_cast<unsigned>(ceil_div(d.d_v, 16)), d.heads, d.nseq), dim3(2 * DK),
                     DeltaJoinCfg<DK>::SMEM, st, p));
   }
   return launch(delta_chunk_kernel<DK, true>, blocks(d.d_v, p.nseg), dim3(32 * warps(d.d_v) + 32),
