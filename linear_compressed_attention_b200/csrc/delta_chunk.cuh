@@ -53,7 +53,7 @@ struct DeltaChunkParams {
   int slots;
   int nseg;           // parts of a sequence's chunks (1: none)
   float* trans;       // [nseq][heads][nseg - 1][d_k][d_v + d_k]: a part's [added state | transition]
-  float* starts;      // [nseq][heads][nseg - 1][d_k][d_v]: the state before parts 1 ..
+  float* starts;      // [nseq][heads][nseg][d_k][d_v]: the state before each part
 };
 
 // Power of two that brings |m| below 2 (down), and its inverse.
@@ -466,8 +466,10 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
   const long head = static_cast<long>(seq) * d.heads + h;
   const float* start = nullptr;
   if (OUT)
-    start = seg == 0 ? (d.state_in ? d.state_in + head * d.d_k * d.d_v : nullptr)
-                     : p.starts + (head * (p.nseg - 1) + seg - 1) * d.d_k * d.d_v;
+    // (with parts, the first's too: the last part's block may be done with state_out, the same buffer, before the
+    // first's begins)
+    start = p.nseg > 1 ? p.starts + (head * p.nseg + seg) * d.d_k * d.d_v
+                       : (d.state_in ? d.state_in + head * d.d_k * d.d_v : nullptr);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -690,8 +692,8 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
   }
 }
 
-// The state before each part: starts[0] = B_0 + M_0 state_in, starts[s] = B_s +
-// M_s starts[s - 1] (fp32). One block for 16 columns of one (sequence, head); a
+// The state before each part: starts[0] = state_in, starts[s + 1] = B_s + M_s
+// starts[s] (fp32). One block for 16 columns of one (sequence, head); a
 // thread sums half of the products of 4 x 4 values (the steps are dependent, so
 // their latency is the time: 5.3 us a step with whole sums, 128 x 128); the next
 // part's M is fetched while this one's is used.
@@ -734,6 +736,8 @@ __global__ void __launch_bounds__(2 * DK) delta_join_kernel(const DeltaChunkPara
     if (d.state_in && in && r0 + i < d.d_k)
       a = *reinterpret_cast<const float4*>(d.state_in + (head * d.d_k + r0 + i) * d.d_v + col0 + x0);
     if (half == 0) *reinterpret_cast<float4*>(sS + (r0 + i) * 16 + x0) = a;
+    if (in && r0 + i < d.d_k)
+      *reinterpret_cast<float4*>(p.starts + (head * p.nseg * d.d_k + r0 + i) * d.d_v + col0 + x0) = a;
   }
   for (int s = 0; s + 1 < p.nseg; ++s) {
     const float* tr = p.trans + (head * (p.nseg - 1) + s) * d.d_k * cols + col0 + x0;
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(2 * DK) delta_join_kernel(const DeltaChunkPara
         *reinterpret_cast<float4*>(sH + (r0 + i) * 16 + x0) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     }
     __syncthreads();
-    float* to = p.starts + (head * (p.nseg - 1) + s) * d.d_k * d.d_v + col0 + x0;
+    float* to = p.starts + (head * p.nseg + s + 1) * d.d_k * d.d_v + col0 + x0;
     if (half == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

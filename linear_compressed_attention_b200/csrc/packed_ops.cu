@@ -264,6 +264,7 @@ struct DeltaPlan {
 int delta_nseg(const edit_delta_rule* a, int64_t chunks, int sms) {
   const int64_t heads = static_cast<int64_t>(a->nseq) * a->heads;
   const int64_t b1 = heads * ceil_div(a->d_v + a->d_k, kDeltaCols), b2 = heads * ceil_div(a->d_v, kDeltaCols);
+  chunks = chunks < 1024 ? chunks : 1024;  // (longer ones as these: the workspace query asks for each length up to it)
   int best = 1;
   double least = static_cast<double>(ceil_div(b2, sms)) * chunks;
   for (int n = 2; n <= kDeltaMaxSeg; ++n) {
@@ -293,7 +294,7 @@ void delta_plan(const edit_delta_rule* a, DeltaPlan& pl) {
   pl.blobs = take(static_cast<size_t>(pl.slots) * a->heads * kDeltaBlob);
   pl.kq = take(static_cast<size_t>(pl.slots) * a->qk_heads * delta_kq_bytes(pl.DK));
   pl.trans = take(heads * (pl.nseg - 1) * a->d_k * (a->d_v + a->d_k) * 4);
-  pl.starts = take(heads * (pl.nseg - 1) * a->d_k * a->d_v * 4);
+  pl.starts = take(pl.nseg > 1 ? heads * pl.nseg * a->d_k * a->d_v * 4 : 0);
 }
 
 template <int DK>
@@ -441,7 +442,7 @@ size_t edit_delta_rule_workspace_bytes(const edit_delta_rule* a) {
     const int n = delta_nseg(a, c, device_sms());
     most = n > most ? n : most;
   }
-  const size_t heads = static_cast<size_t>(a->nseq) * a->heads, more = most > pl.nseg ? most - pl.nseg : 0;
+  const size_t heads = static_cast<size_t>(a->nseq) * a->heads, more = most > pl.nseg ? most : 0;
   return pl.total + align256(heads * more * a->d_k * (a->d_v + a->d_k) * 4) + align256(heads * more * a->d_k * a->d_v * 4);
 }
 

@@ -236,3 +236,22 @@ def test_captured_call_replays_with_other_lengths():
         eager = other.forward(q, k, v, g, beta, at, state_out=s2, out=torch.full_like(v, 2.0))
         assert torch.equal(out, eager) and torch.equal(so, s2)
         check(out, so, R.delta_rule(q, k, v, g, beta, now, None, 0.125, True), now)
+
+
+@pytest.mark.parametrize("S,h,lens", [(1, 2, [3000]), (2, 20, [1500, 1100]), (1, 40, [2100])])
+def test_parts_of_long_sequences_and_states_in_place(S, h, lens):
+    # few (sequence, head) pairs: a sequence's chunks are cut into parts that run side by side, more blocks than SMs in
+    # some; the final states may go where the first ones are read
+    at = offsets(lens)
+    q, k, v, g, beta = inputs(21, "bf16", at[-1], h // 2, h, 128, 128, rate=0.02)
+    state = torch.randn(S, h, 128, 128, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    op = bd.DeltaRule(h // 2, h, 128, 128, S, at[-1], "bf16")
+    apart = torch.zeros_like(state)
+    out = op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=apart)
+    assert op.status() == 0
+    for _ in range(3):
+        same = state.clone()
+        assert torch.equal(op.forward(q, k, v, g, beta, ints(at), state_in=same, state_out=same), out)
+        assert torch.equal(same, apart)
+    if h <= 4:
+        check(out, apart, R.delta_rule(q, k, v, g, beta, at, state, 128 ** -0.5, True), at)
