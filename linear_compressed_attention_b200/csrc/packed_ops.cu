@@ -68,7 +68,10 @@ struct AttnPlan {
 };
 
 // bf16 calls whose sequences have at most 128 packed rows on average take one
-// row tile a block and two blocks an SM, others two row tiles a block.
+// row tile a block and two blocks an SM, others two row tiles a block, which halves
+// the keys read (8 sequences over 2048 keys, 16 heads of 128, us with one / two: 32
+// rows 46 / 51, 128 rows 68 / 82, 256 rows 112 / 114; 4 x 4096 rows over 333 keys, 16
+// heads of 72: 90 / 79).
 int attn_row_tiles(const edit_packed_attention* a, int64_t rows) {
   return rows * (a->heads / a->kv_heads) <= 128 * static_cast<int64_t>(a->nseq) ? 1 : 2;
 }
@@ -231,22 +234,23 @@ int delta_recurrent(const DeltaParams& p, cudaStream_t st) {
   return launch(delta_recurrent_kernel<T, 128, STEP>, grid, block, 0, st, p, cb);
 }
 
-// Single tokens: whole states through shared memory where two blocks for every SM
-// are there to bring them in, else smaller blocks.
+// Single tokens: whole states through shared memory where most SMs get one, else
+// smaller blocks (16 heads of 128 x 128, us: 4 sequences 5.5 against 4.5, 8: 5.7 /
+// 6.8, 16: 7.6 / 11.3, 32: 13.3 / 20.2; with d_v = 64 the two are the same, 7.3 /
+// 6.9 for 32 sequences).
 template <typename T>
 int delta_single(const DeltaParams& p, cudaStream_t st) {
   const long blocks = static_cast<long>(p.nseq) * p.heads;
-  const size_t bytes = static_cast<size_t>(p.d_k) * p.d_v * 4;
-  if (blocks >= 2L * device_sms()) {
-    const dim3 grid(static_cast<unsigned>(p.nseq), p.heads), block(256);
-    if (p.d_v == 128) return launch(delta_step_kernel<T, 128>, grid, block, bytes, st, p);
-    if (p.d_v == 64) return launch(delta_step_kernel<T, 64>, grid, block, bytes, st, p);
-  }
+  if (p.d_v == 128 && 4 * blocks >= 3L * device_sms())
+    return launch(delta_step_kernel<T, 128>, dim3(static_cast<unsigned>(p.nseq), p.heads), dim3(256),
+                  static_cast<size_t>(p.d_k) * 128 * 4, st, p);
   return delta_recurrent<T, true>(p, st);
 }
 
 // bf16 calls with sequences of at least this many rows on average run in chunks
-// of 64 tokens, others token by token.
+// of 64 tokens, others token by token (16 heads of 128, us for 64 sequences of 16 /
+// 32 / 64 tokens: 133 / 136 / 140 in chunks, 96 / 163 / 298 token by token; one
+// sequence: 22 / 22 / 23 and 9 / 15 / 28).
 constexpr int kDeltaChunkedRows = 32;
 
 struct DeltaPlan {
