@@ -3,7 +3,7 @@
 //   r = x + rho act(gate) N_post(y),  h = N_pre(r) (1 + scale) + shift
 // The row stays in registers between the reads of x, y and the writes of r, h,
 // so that both norms cost no memory traffic: 4 C values a row, which bounds it
-// (65536 rows of 1152 bf16 are 604 MB, 92 us at the copy rate).
+// (65536 rows of 1152 bf16 are 604 MB, 92 us at the copy rate; it takes 108).
 #pragma once
 
 #include "packed_seq.cuh"
