@@ -5,9 +5,19 @@ round to bf16, and (n + c) 2^-24 of the sum of absolute terms for an fp32 sum of
 n terms."""
 import math
 
+import pytest
 import torch
 
 U32 = 2.0 ** -24
+
+
+@pytest.fixture(autouse=True)
+def float32_default():
+    """fp32 for tensors made without a type, whatever another test module has set."""
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(was)
 
 
 def half_step(dtype):
@@ -73,7 +83,7 @@ def delta_rule(q, k, v, g, beta, at, state, scale, norm, eps=1e-6):
     # bf16 inputs may run on operands split into two bf16 halves, 2^-16 of each of the three products in a row
     c = (dk + 64 + 16) * U32 + bf * 3 * 2.0 ** -16
     for s in range(n):
-        us = []
+        us, before = [], []
         for t in range(at[s], at[s + 1]):
             a = gd[t].exp()
             kt, qt = kd[t], qd[t]
@@ -85,18 +95,21 @@ def delta_rule(q, k, v, g, beta, at, state, scale, norm, eps=1e-6):
             E[s] = a * E[s] + c * (size + kn * bd[t] * (vd[t].norm(dim=-1) + kn * size))
             S[s] = S[s] + kt[:, :, None] * u[:, None, :]
             out[t] = scale * torch.einsum("hk,hkv->hv", qt, S[s])
-            us.append((t, kt, u.norm(dim=-1)))
-            us = us[-64:]
+            us.append(u.norm(dim=-1))
+            before.append(size + E[s])
             ob[t] = half_step(q.dtype) * out[t].norm(dim=-1) + scale * qn * (E[s] + c * S[s].flatten(1).norm(dim=1))
-            if bf:  # the products that give the output may take state, scores and values rounded to bf16
-                recent = torch.zeros_like(size)
-                for j, kj, un in us:
-                    recent += (gd[j + 1:t + 1].sum(0)).exp() * (qt * kj).sum(-1).abs() * un
-                ob[t] += scale * 2.0 ** -8 * (qn * (size + E[s]) + 2.1 * recent)
-                # the chunk's first state decays to `size` in the bound above only if no value left it since: add what
-                # the chunk's own tokens may have taken out
-                for j, kj, un in us:
-                    ob[t] += scale * 2.0 ** -8 * qn * (gd[j + 1:t + 1].sum(0)).exp() * un * kj.norm(dim=-1)
+        if bf and us:  # the products that give the output may take state, scores and values rounded to bf16
+            r = slice(at[s], at[s + 1])
+            G, un, n_t = gd[r].cumsum(0), torch.stack(us), len(us)          # [T, H]
+            lag = torch.arange(n_t, device=v.device)[:, None] - torch.arange(n_t, device=v.device)
+            near = ((lag >= 0) & (lag < 64))[None]                          # a chunk's tokens up to this one
+            D = torch.where(near, G.T[:, :, None] - G.T[:, None, :], -math.inf).exp() * un.T[:, None, :]   # [H, t, j]
+            qk = torch.einsum("thk,jhk->htj", qd[r], kd[r]).abs()
+            qn = qd[r].norm(dim=-1)
+            ob[r] += scale * 2.0 ** -8 * (qn * torch.stack(before) + 2.1 * (D * qk).sum(-1).T)
+            # a chunk's first state decays to `size` in the bound above only if no value left it since: add what the
+            # chunk's own tokens may have taken out
+            ob[r] += scale * 2.0 ** -8 * qn * (D * kd[r].norm(dim=-1).T[:, None, :]).sum(-1).T
     return out, S, ob + 1e-30, E + 1e-30
 
 

@@ -5,6 +5,7 @@ import torch
 
 import packed_ref as R
 from linear_compressed_attention_b200 import binding as bd
+from packed_ref import float32_default  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
