@@ -527,13 +527,25 @@ class DitBlock:
 
 
 # ----------------------------------------------------------- packed sequences
+def _addr(t):
+    """A tensor's address for an argument of type void* (an int, as cheap as it gets: these calls may be short)."""
+    return None if t is None else t.data_ptr()
+
+
+def _handle(stream):
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
 def edit_packed_attention_workspace_bytes(args: PackedAttentionArgs) -> int:
     return int(lib().edit_packed_attention_workspace_bytes(ctypes.byref(args)))
 
 
 def edit_packed_attention_forward(q, k, v, args: PackedAttentionArgs, out, stream=None) -> int:
-    return int(lib().edit_packed_attention_forward(_ptr(q), _ptr(k), _ptr(v), ctypes.byref(args), _ptr(out),
-                                                   _stream(stream)))
+    return int(lib().edit_packed_attention_forward(_addr(q), _addr(k), _addr(v), ctypes.byref(args), _addr(out),
+                                                   _handle(stream)))
 
 
 def edit_delta_rule_workspace_bytes(args: DeltaRuleArgs) -> int:
@@ -541,32 +553,33 @@ def edit_delta_rule_workspace_bytes(args: DeltaRuleArgs) -> int:
 
 
 def edit_delta_rule_forward(q, k, v, g, beta, args: DeltaRuleArgs, state_in, state_out, out, stream=None) -> int:
-    return int(lib().edit_delta_rule_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.byref(args),
-                                             _ptr(state_in), _ptr(state_out), _ptr(out), _stream(stream)))
+    return int(lib().edit_delta_rule_forward(_addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), ctypes.byref(args),
+                                             _addr(state_in), _addr(state_out), _addr(out), _handle(stream)))
 
 
 def edit_delta_rule_step(q, k, v, g, beta, args: DeltaRuleArgs, state, out, stream=None) -> int:
-    return int(lib().edit_delta_rule_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.byref(args),
-                                          _ptr(state), _ptr(out), _stream(stream)))
+    return int(lib().edit_delta_rule_step(_addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), ctypes.byref(args),
+                                          _addr(state), _addr(out), _handle(stream)))
 
 
 def edit_block_norm_forward(x, y, args: BlockNormArgs, r_out, h_out, stream=None) -> int:
-    return int(lib().edit_block_norm_forward(_ptr(x), _ptr(y), ctypes.byref(args), _ptr(r_out), _ptr(h_out),
-                                             _stream(stream)))
+    return int(lib().edit_block_norm_forward(_addr(x), _addr(y), ctypes.byref(args), _addr(r_out), _addr(h_out),
+                                             _handle(stream)))
 
 
 def _check_rows(name, t, dtype, shape, device):
     """A device tensor of rows whose other dimensions are contiguous; returns its row stride."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} is not on the current device")
-    st = t.stride()
+    width = shape[1] * shape[2] if len(shape) == 3 else shape[1]
     if shape[0] == 0:
-        return int(np.prod(shape[1:]))
+        return width
+    st = t.stride()
     if st[-1] != 1 and shape[-1] > 1 or (len(st) == 3 and st[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: only the rows may be strided")
-    return st[0] if shape[0] > 1 else int(np.prod(shape[1:]))
+    return st[0] if shape[0] > 1 else width
 
 
 def _check_ints(name, t, n, device):
@@ -659,7 +672,7 @@ class DeltaRule(_Packed):
         return n, dev, out
 
     def _state(self, name, t, dev):
-        if t is not None and (t.dtype != self.torch.float32 or tuple(t.shape) != self.state_shape or
+        if t is not None and (t.dtype != self.torch.float32 or t.shape != self.state_shape or
                               not t.is_contiguous() or t.get_device() != dev):
             raise ValueError(f"{name}: contiguous float32 {self.state_shape} on the current device expected")
 
