@@ -339,8 +339,10 @@ int norm_rows(const BlockNormParams& p, cudaStream_t st) {
 }
 
 // Threads a row: a warp where its registers hold the row (40 values a thread in
-// bf16, 16 in fp32, which fills an SM with warps all the same), else 128 or 256;
-// a block's all for rows without 16-byte vectors or few of them.
+// bf16, 16 in fp32, which fills an SM with warps all the same), two for wider bf16
+// rows (30000 rows of 1536: 67 us, with four 82; fp32 the other way, 133 / 124), four
+// for the others and where rows are few; a block's all for rows without 16-byte
+// vectors.
 template <typename T>
 int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
   if (p.C > kBnNarrow) {
@@ -358,6 +360,8 @@ int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
       if (nv <= 160) return norm_rows<T, 8, 32, 5>(p, st);
     }
   }
+  if (sizeof(T) == 2 && nv > 160 && p.rows > 2L * device_sms())
+    return nv <= 192 ? norm_rows<T, 8, 64, 3>(p, st) : norm_rows<T, 8, 64, 4>(p, st);
   return nv <= 128 ? norm_rows<T, 8, 128, 1>(p, st) : norm_rows<T, 8, 128, 2>(p, st);
 }
 
