@@ -144,3 +144,36 @@ def test_captured_call_and_no_rows():
     assert torch.equal(r, want[0]) and (r[31:] == 4.0).all()
     e = x[:0]
     assert op.forward(e, e, gate=m, offsets=ints([0, 0, 0]))[0].shape == (0, 1152)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [64, 300, 504, 768, 1000, 1152, 1288, 1536, 1999, 2048, 2304])
+def test_many_rows(dtype, C):
+    # enough rows for every layout of a row over threads; samples that begin and end inside a block's rows, and none
+    n, at = 1500, [4, 5, 5, 600, 1203, 1497]
+    x, y = rand(31, dtype, n, C), rand(32, dtype, n, C, gain=2.0)
+    mod = rand(33, dtype, 5, 3, C, gain=0.5)
+    w = rand(34, dtype, C, mean=1.0, gain=0.2)
+    op = bd.BlockNorm(C, dtype, post="layer", pre="rms", gate_act="tanh", post_w=w, pre_b=w)
+    r, h = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+    op.forward(x, y, gate=mod[:, 0], scale=mod[:, 1], shift=mod[:, 2], offsets=ints(at), r_out=r, h_out=h)
+    sample = torch.bucketize(torch.arange(4, 1497, device="cuda"), torch.tensor(at[1:], device="cuda"), right=True)
+    ref = R.block_norm(x[4:1497], y[4:1497], sample, "layer", "rms", "tanh", 1e-6, 1.0,
+                       dict(post_w=w, pre_b=w, gate=mod[:, 0], scale=mod[:, 1], shift=mod[:, 2]))
+    check(r[4:1497], ref[0], ref[2])
+    check(h[4:1497], ref[1], ref[3])
+    for t in (r, h):
+        assert (t[:4] == 9.0).all() and (t[1497:] == 9.0).all()
+    r2, h2 = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+    op.forward(x, y, gate=mod[:, 0], scale=mod[:, 1], shift=mod[:, 2], offsets=ints(at), r_out=r2, h_out=h2)
+    assert torch.equal(r, r2) and torch.equal(h, h2)
+
+
+def test_one_sample_a_row():
+    n, C = 900, 264
+    x, y, m = rand(41, "bf16", n, C), rand(42, "bf16", n, C), rand(43, "bf16", n, C)
+    r, h = bd.BlockNorm(C, "bf16", post="rms", pre="layer").forward(x, y, gate=m, scale=m, shift=m)
+    ref = R.block_norm(x, y, torch.arange(n, device="cuda"), "rms", "layer", "linear", 1e-6, 1.0,
+                       dict(gate=m, scale=m, shift=m))
+    check(r, ref[0], ref[2])
+    check(h, ref[1], ref[3])

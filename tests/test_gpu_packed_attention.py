@@ -255,3 +255,27 @@ def test_two_calls_at_once_have_workspaces_of_their_own():
             op.forward(q, k, v, qo, ko, out=o, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and lens
+
+
+@pytest.mark.parametrize("S,heads,n,d", [(500, 16, 3, 32), (230, 16, 130, 64)])
+def test_many_sequences(S, heads, n, d):
+    # more items than a block finds at a time; short and longer row tiles, one of every seven sequences empty
+    lens = [0 if s % 7 == 3 else n for s in range(S)]
+    if n > 100:
+        lens = [n + 21 if m else 0 for m in lens]
+    run("bf16", heads, heads, d, lens, lens, True, seed=6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_new_tokens_do_not_see_what_comes_after_them(dtype, where):
+    # three new tokens over a split cache; what is not finite lies in the last key, which only the last of them sees
+    H, K, d, n = 8, 2, 64, 3001
+    q, k, v = draw(90, dtype, 3, H, d), draw(91, dtype, n, K, d), draw(92, dtype, n, K, d)
+    ref, bound = R.attention(q, k, v, [0, 3], [0, n], None, True, d ** -0.5)
+    (k if where == "k" else v)[n - 1, 0, 5] = float("nan")
+    op = bd.PackedAttention(H, K, d, 1, 3, n, dtype, causal=True)
+    out = op.forward(q, k, v, ints([0, 3]), ints([0, n])).double()
+    ok = (out - ref).abs() <= bound
+    assert ok[:2].all() and ok[2, H // 2:].all()
+    assert torch.isnan(out[2, :H // 2, 5]).all()
