@@ -341,15 +341,22 @@ int norm_rows(const BlockNormParams& p, cudaStream_t st) {
 // Threads a row: a warp where its registers hold the row (40 values a thread in
 // bf16, 16 in fp32, which fills an SM with warps all the same), two for wider bf16
 // rows (30000 rows of 1536: 67 us, with four 82; fp32 the other way, 133 / 124), four
-// for the others and where rows are few; a block's all for rows without 16-byte
-// vectors.
+// for the others and where rows are few. Rows without 16-byte vectors: 16 values a
+// thread where there are rows enough (20000 rows of 1001 bf16 130 us, with 4 or 8
+// values 172; fp32 63 / 106), which is bound by its 2- and 4-byte accesses.
 template <typename T>
 int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
   if (p.C > kBnNarrow) {
     if (!vec) return norm_launch<T, 1, 256, 64>(p, st);
     return p.C <= 4096 ? norm_launch<T, 8, 256, 2>(p, st) : norm_launch<T, 8, 256, 8>(p, st);
   }
-  if (!vec) return p.C <= 512 ? norm_rows<T, 1, 128, 4>(p, st) : norm_rows<T, 1, 256, 8>(p, st);
+  if (!vec) {
+    if (p.rows <= 2L * device_sms()) return p.C <= 512 ? norm_rows<T, 1, 128, 4>(p, st) : norm_rows<T, 1, 256, 8>(p, st);
+    if (p.C <= 256) return norm_rows<T, 1, 32, 8>(p, st);
+    if (p.C <= 512) return norm_rows<T, 1, 32, 16>(p, st);
+    if (p.C <= 1024) return norm_rows<T, 1, 64, 16>(p, st);
+    return norm_rows<T, 1, 128, 16>(p, st);
+  }
   const int nv = p.C / 8;
   if (p.rows > 2L * device_sms()) {
     if (nv <= 32) return norm_rows<T, 8, 32, 1>(p, st);
