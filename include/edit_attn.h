@@ -455,7 +455,8 @@ EDIT_API int edit_linear_attention_noalloc(const void *q, const void *k, const v
  *   Head groups: heads is a multiple of kv_heads (or qk_heads); head h reads
  *             the shared head h / (heads / kv_heads).
  *   Outputs must not overlap the inputs unless a function says so. Tensors of
- *   no rows may be NULL. All memory belongs to the current device. */
+ *   no rows may be NULL. All memory belongs to the current device, whose SM
+ *   count the plans read (query the workspace with that device current). */
 
 /* Softmax attention over packed sequences. For row i (0-based) of a sequence
  * with a query rows and b keys, and per head:
