@@ -256,3 +256,19 @@ def test_parts_of_long_sequences_and_states_in_place(S, h, lens):
         assert torch.equal(same, apart)
     if h <= 4:
         check(out, apart, R.delta_rule(q, k, v, g, beta, at, state, 128 ** -0.5, True), at)
+
+
+@pytest.mark.parametrize("at", [[0, 200, 100], [150, 20, 200], [-3, 100, 200], [0, 100, 500], [2 ** 31 - 1, -2 ** 31, 7]])
+def test_bad_offsets_of_chunked_calls(at):
+    # long enough for the chunked kernels: every slot they read lies in the workspace whatever the offsets are
+    q, k, v, g, beta = inputs(23, "bf16", 200, 1, 2, 64, 64)
+    guard = torch.full((204, 2, 64), 5.0, device="cuda", dtype=torch.bfloat16)
+    op = bd.DeltaRule(1, 2, 64, 64, 2, 200, "bf16")
+    op.workspace.zero_()
+    so = torch.zeros(2, 2, 64, 64, device="cuda")
+    op.forward(q, k, v, g, beta, ints(at), state_out=so, out=guard[2:202])
+    assert op.status() == -2
+    assert (guard[:2] == 5.0).all() and (guard[202:] == 5.0).all()
+    out = op.forward(q, k, v, g, beta, ints([0, 100, 200]), state_out=so)
+    assert op.status() == 0
+    check(out, so, R.delta_rule(q, k, v, g, beta, [0, 100, 200], None, 0.125, True), [0, 100, 200])
