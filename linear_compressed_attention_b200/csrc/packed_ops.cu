@@ -380,7 +380,9 @@ size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
   if (attn_args(a) != EDIT_OK) return 0;
   // Fewer rows can mean more parts: the most over all row counts up to rows_q and
   // both tile heights. Rows with the same number of slots have the same parts, so
-  // the last of each are enough.
+  // the last of each are enough, and more slots never have more parts (no rows at
+  // all have one part whatever the slots: with one row a tile the scan meets them
+  // first, and goes on).
   size_t most = kStatusBytes;
   const int G = a->heads / a->kv_heads;
   const int heights[2] = {a->dtype == EDIT_BF16 ? 128 / G : 64 / G, a->dtype == EDIT_BF16 ? 2 * (128 / G) : 64 / G};
@@ -389,7 +391,7 @@ size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
       AttnPlan pl;
       attn_plan(a, rows < a->rows_q ? rows : a->rows_q, R, pl);
       if (pl.total > most) most = pl.total;
-      if (pl.nsplit == 1 || rows >= a->rows_q) break;
+      if ((pl.nsplit == 1 && rows > 0) || rows >= a->rows_q) break;
     }
   }
   return most;

@@ -279,3 +279,11 @@ def test_new_tokens_do_not_see_what_comes_after_them(dtype, where):
     ok = (out - ref).abs() <= bound
     assert ok[:2].all() and ok[2, H // 2:].all()
     assert torch.isnan(out[2, :H // 2, 5]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [33, 64])
+def test_many_heads_on_one_key_head_with_split_keys(dtype, heads):
+    # more than 32 query heads a key/value head: one row a tile of the fp32 kernel; the workspace is the query's
+    run(dtype, heads, 1, 64, [3], [4500], True, seed=7)
+    run(dtype, heads, 1, 64, [1, 0, 2], [2100, 5, 3000], False, seed=8, behind=0)

@@ -3,6 +3,7 @@ documented codes, before touching the device (no GPU here)."""
 import ctypes
 
 import pytest
+import torch
 
 from linear_compressed_attention_b200 import binding as bd
 
@@ -57,6 +58,27 @@ def test_attention_null_struct_and_workspace_query():
         assert need == sorted(need) and need[-1] <= most
     # the split itself: few rows over a long cache take more than the status block
     assert bd.edit_packed_attention_workspace_bytes(attn(rows_q=1, nseq=1, max_k=100000)) > 4096
+
+# For calls whose arguments are all in order and whose addresses are not: past the checks the launch fails for want of
+# a device, with a code of its own; never run where there is one.
+no_device = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
+
+
+@no_device
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("kv,group", [(1, 1), (2, 3), (8, 4), (1, 32), (1, 33), (2, 40), (1, 64)])
+def test_attention_workspace_serves_every_smaller_call(dtype, kv, group):
+    # group 33 to 64: a tile of the fp32 kernel holds one row, and its query met the plan of no rows first
+    for nseq in (1, 3, 40):
+        for max_k in (0, 257, 8192):
+            kw = dict(dtype=dtype, heads=kv * group, kv_heads=kv, nseq=nseq, max_k=max_k, rows_k=0, ldq=kv * group * 64,
+                      ldo=kv * group * 64, ldk=kv * 64, ldv=kv * 64, k=0, v=0)
+            query = {n: v for n, v in kw.items() if n not in ("k", "v")}
+            for most in (1, 4, 100, 700):
+                room = bd.edit_packed_attention_workspace_bytes(attn(rows_q=most, **query))
+                for rows in {1, 2, 3, most // 3, most // 2, most - 1, most}:
+                    if 1 <= rows <= most:
+                        assert attn_call(rows_q=rows, workspace_bytes=room, **kw) != WORKSPACE
 
 
 def delta(**kw):
