@@ -1,5 +1,9 @@
 """The gated delta rule through the C ABI against the token-by-token 64-bit
 form, within the bounds of packed_ref.delta_rule."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -272,3 +276,36 @@ def test_bad_offsets_of_chunked_calls(at):
     out = op.forward(q, k, v, g, beta, ints([0, 100, 200]), state_out=so)
     assert op.status() == 0
     check(out, so, R.delta_rule(q, k, v, g, beta, [0, 100, 200], None, 0.125, True), [0, 100, 200])
+
+
+WIDTHS_OF_WHOLE_STATES = """
+import torch
+from linear_compressed_attention_b200 import binding as bd
+S, h, dv = 24, 16, 128
+for dt, name in ((torch.bfloat16, "bf16"), (torch.float32, "f32")):
+    q, k = (torch.ones(S, h, {dk}, device="cuda", dtype=dt) for _ in "qk")
+    v = torch.ones(S, h, dv, device="cuda", dtype=dt)
+    z, state = torch.zeros(S, h, device="cuda"), torch.zeros(S, h, {dk}, dv, device="cuda")
+    out = bd.DeltaRule(h, h, {dk}, dv, S, 0, name, scale=1.0, qk_norm=False).step(q, k, v, z, z + 1, state)
+    assert (state == 1).all() and (out == {dk}).all()
+"""
+
+
+@pytest.mark.parametrize("dk", [88, 96, 104])
+def test_whole_states_in_a_process_that_ran_no_wider_ones(dk):
+    # a state of 96 x 128 fills 48 KB of dynamic shared memory to the byte, and the kernel has static memory besides;
+    # the limit is the process's: once raised for a wider state it would serve this one too
+    root = os.path.dirname(os.path.dirname(os.path.abspath(bd.__file__)))
+    subprocess.run([sys.executable, "-c", WIDTHS_OF_WHOLE_STATES.format(dk=dk)], cwd=root, check=True, timeout=300)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk", [24, 88, 96, 120])
+def test_step_of_whole_states_of_other_widths(dtype, dk):
+    S, hq, h, dv = 24, 8, 16, 128
+    q, k, v, g, beta = inputs(31, dtype, S, hq, h, dk, dv)
+    state = torch.randn(S, h, dk, dv, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    op = bd.DeltaRule(hq, h, dk, dv, S, 0, dtype, scale=0.7)
+    mine = state.clone()
+    out = op.step(q, k, v, g, beta, mine)
+    check(out, mine, R.delta_rule(q, k, v, g, beta, list(range(S + 1)), state, 0.7, True), [0, S])
