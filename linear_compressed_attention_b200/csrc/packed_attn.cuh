@@ -68,8 +68,9 @@ __device__ __forceinline__ bool attn_item(const PackedAttnParams& p, int slot, i
 // ---------------------------------------------------------------- CUDA cores
 // 64 packed rows against 64 keys at a time; a thread holds 4 rows x 4 keys of
 // the scores and 4 rows x DP / 16 columns of the output. K and V rows past the
-// visible keys are zeros in shared memory, and a masked weight skips its
-// product, so that nothing behind a mask reaches a row.
+// visible keys are zeros in shared memory, and a masked key skips its product, so
+// that nothing behind a mask reaches a row (a key that is seen never does: a weight
+// of 0 times what is not finite is NaN, whichever tile the key lies in).
 template <typename T, int DP>
 __global__ void __launch_bounds__(256) packed_attn_simt_kernel(const PackedAttnParams p) {
   pdl_wait();
@@ -174,6 +175,9 @@ __global__ void __launch_bounds__(256) packed_attn_simt_kernel(const PackedAttnP
         for (int w = 0; w < CW; ++w) o[i][j][w] *= alpha;
     }
     masked = __syncthreads_or(masked);
+    int n[4];  // visible keys of this tile
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = see[i] - key0;
     auto accumulate = [&](auto skip) {
 #pragma unroll 4
       for (int key = 0; key < nk; ++key) {
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(256) packed_attn_simt_kernel(const PackedAttnP
             const float x = sv[key * DP + 64 * j + tx * CW + w];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (!decltype(skip)::value || pr[i] != 0.f) o[i][j][w] = fmaf(pr[i], x, o[i][j][w]);
+              if (!decltype(skip)::value || key < n[i]) o[i][j][w] = fmaf(pr[i], x, o[i][j][w]);
           }
       }
     };

@@ -287,3 +287,21 @@ def test_many_heads_on_one_key_head_with_split_keys(dtype, heads):
     # more than 32 query heads a key/value head: one row a tile of the fp32 kernel; the workspace is the query's
     run(dtype, heads, 1, 64, [3], [4500], True, seed=7)
     run(dtype, heads, 1, 64, [1, 0, 2], [2100, 5, 3000], False, seed=8, behind=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n,nq,j", [(100, 100, 70), (200, 200, 20), (3001, 3, 2999), (3001, 3, 1500)])
+def test_what_is_not_finite_reaches_rows_whose_weight_of_it_is_zero(dtype, bad, n, nq, j):
+    # key j scores 400 below the others: its weight is 0 in fp32, in tiles with masked keys and in others alike
+    H, K, d = 4, 2, 64
+    q, k, v = draw(100, dtype, nq, H, d), draw(101, dtype, n, K, d), draw(102, dtype, n, K, d)
+    q[..., 0], k[..., 0], k[j, :, 0] = 20.0, 0.0, -160.0
+    ref, bound = R.attention(q, k, v, [0, nq], [0, n], None, True, d ** -0.5)
+    v[j, 1, 3] = bad
+    op = bd.PackedAttention(H, K, d, 1, nq, n, dtype, causal=True)
+    out = op.forward(q, k, v, ints([0, nq]), ints([0, n])).double()
+    first = max(0, j - (n - nq))                         # the first row that sees it
+    ok = (out - ref).abs() <= bound
+    assert ok[:first].all() and ok[:, :2].all() and ok[:, :, [c for c in range(d) if c != 3]].all()
+    assert (~torch.isfinite(out[first:, 2:, 3])).all()
