@@ -224,8 +224,14 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
   {
     const int t = tid & 63;
     const float s = (tid < 64 ? sNk : sNq)[t];
-    float down, up;
-    pow2_scale(sqrtf(s), down, up);  // (no value is larger than the norm)
+    float m = sqrtf(s), down, up;  // no value is larger than the norm, where its square has not left fp32's range
+    if (!(s > 1e-30f && s < 1e38f)) {
+      const uint32_t* row = reinterpret_cast<const uint32_t*>((tid < 64 ? sK : sQ) + t * LD);
+      uint32_t most = 0;
+      for (int x = 0; x < DK / 2; ++x) most = max(most, max(row[x] << 16 & 0x7fff0000u, row[x] & 0x7fff0000u));
+      m = __uint_as_float(most);
+    }
+    pow2_scale(m, down, up);
     (tid < 64 ? sRk : sRq)[t] = t >= n ? 0.f : (d.qk_norm ? 1.f / sqrtf(s + d.qk_eps) : 1.f);
     (tid < 64 ? sKd : sQd)[t] = down;
     (tid < 64 ? sKu : sQu)[t] = up;

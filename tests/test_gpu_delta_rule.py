@@ -309,3 +309,37 @@ def test_step_of_whole_states_of_other_widths(dtype, dk):
     mine = state.clone()
     out = op.step(q, k, v, g, beta, mine)
     check(out, mine, R.delta_rule(q, k, v, g, beta, list(range(S + 1)), state, 0.7, True), [0, S])
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("size", [1e-20, 1e-24, 1e-30, 1e-38])
+def test_rows_of_tiny_values_in_chunks(size, which, norm):
+    # rows whose sum of squares is 0 or subnormal in fp32 and whose values are not 0
+    n, at = 200, [0, 200]
+    q, k, v, g, beta = inputs(41, "bf16", n, 1, 2, 64, 64, rate=0.05)
+    if not norm:
+        q, k = ((0.98 * x.float() / x.float().norm(dim=-1, keepdim=True)).to(x.dtype) for x in (q, k))
+    x = q if which == "q" else k
+    for t in (0, 10, 70, 71, 72, 199):
+        x[t] = (size * x[t].float()).to(x.dtype)
+    x[100] = 0
+    x[100, 0, 5] = size
+    state = torch.randn(1, 2, 64, 64, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    op = bd.DeltaRule(1, 2, 64, 64, 1, n, "bf16", qk_norm=norm)
+    so = torch.zeros_like(state)
+    out = op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=so)
+    check(out, so, R.delta_rule(q, k, v, g, beta, at, state, 0.125, norm), at)
+
+
+def test_rows_of_huge_queries_in_chunks():
+    # queries as given whose sum of squares is past fp32: their outputs are finite
+    n, at = 130, [0, 130]
+    q, k, v, g, beta = inputs(42, "bf16", n, 1, 2, 64, 64, rate=0.05)
+    k = (0.98 * k.float() / k.float().norm(dim=-1, keepdim=True)).to(k.dtype)
+    q[[3, 64, 129]] *= 1e21
+    state = torch.randn(1, 2, 64, 64, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    op = bd.DeltaRule(1, 2, 64, 64, 1, n, "bf16", qk_norm=False)
+    so = torch.zeros_like(state)
+    out = op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=so)
+    check(out, so, R.delta_rule(q, k, v, g, beta, at, state, 0.125, False), at)
