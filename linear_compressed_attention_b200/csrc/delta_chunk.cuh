@@ -19,14 +19,22 @@
 // us in 9 parts: inverses 67, effects of the parts 152, join 36, walk 112; the walks
 // are bound by mma.sync and its operands' splitting, about 5 us a chunk of 8 warps.
 //
-// Precision: the state is fp32, and what flows into it keeps fp32's precision
-// on fp16 operands: an fp32 operand row is scaled by a power of two to below 2
-// and split into two fp16 halves (22 bits), k (8 bits) is exact in fp16 after
-// such a scaling, and T is split as well; the dropped product of two low halves
-// is 2^-22. (Two bf16 halves would leave 2^-17 and three would cost half as many
-// products again.) O is rounded to bf16, so Q^ S0 takes one fp16 half, and P U,
-// whose terms a decay may set many powers of two apart, P in bf16 and U in two
-// bf16 halves (with U in one, O was 1.5 times as far off as its own rounding).
+// Precision: the state is fp32. Its products take fp16 operands: a column of the
+// state (of the decayed U in the state's sum) is scaled by a power of two to
+// below 2 and split into two fp16 halves, a row of k likewise but in one half;
+// errors are 2^-22 of the column's largest value (the dropped part, and the fp16
+// floor of 2^-25 below the scale), as much of k's row for its values below 2^-15 of
+// the largest. (Two bf16 halves would leave 2^-17 and three would cost half as many
+// products again.) U = T X takes three bf16 parts of each, six products and 2^-24
+// of each term: there the tokens of a chunk meet, and with one scale for all of them
+// a large value, even of a later token or of a state since forgotten, rounded small
+// ones away (with three products of fp16 halves the walks were 5% shorter). O is
+// rounded to bf16, so Q^ S0 takes one fp16 half, 2^-12 of the column's largest value
+// for each term, and P U, whose terms a decay may set many powers of two apart, P in
+// bf16 and U in two bf16 halves (with U in one, O was 1.5 times as far off as its own
+// rounding).
+// Values that are not finite reach what comes after them and nothing before: see
+// `cut` in the walk, and the zeros above diagonals that the inverse skips.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -38,13 +46,16 @@
 namespace edit {
 
 constexpr int kDeltaL = 64;    // tokens a chunk
-constexpr int kDeltaLd = 72;   // row stride (fp16) of T and P: 16-byte rows without bank conflicts
 
-// Per (chunk slot, head): T high, T low [64][72] fp16, the scalars, P [64][72] bf16.
-enum { DS_FX, DS_T, DS_W, DS_FO, DS_A, DS_COUNT };  // rows of 64 fp32 scalars
-constexpr int kDeltaMat = kDeltaL * kDeltaLd * 2;
+// Lower triangles (T, P) are kept by 16-row blocks: rows of block t have the 16 (t + 1) columns up to the diagonal
+// block and 8 of padding (16-byte rows without bank conflicts).
+__host__ __device__ constexpr int delta_tri_ld(int t) { return 16 * t + 24; }
+__host__ __device__ constexpr int delta_tri_at(int t) { return 128 * t * (t + 2); }  // first value of block t
+constexpr int kDeltaMat = delta_tri_at(kDeltaL / 16) * 2;
+// Per (chunk slot, head): T in three bf16 parts, the scalars, P in bf16.
+enum { DS_FX, DS_W, DS_FO, DS_A, DS_COUNT };  // rows of 64 fp32 scalars
 constexpr int kDeltaScal = DS_COUNT * kDeltaL * 4;
-constexpr int kDeltaBlob = 3 * kDeltaMat + kDeltaScal;
+constexpr int kDeltaBlob = 4 * kDeltaMat + kDeltaScal;
 // Per (chunk slot, qk head): K, Q [64][DK + 8] fp16, each row scaled to below 2.
 __host__ __device__ constexpr int delta_kq_bytes(int DK) { return 2 * kDeltaL * (DK + 8) * 2; }
 
@@ -76,6 +87,15 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   const float2 f = __half22float2(h);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = pack_f16x2(x0 - f.x, x1 - f.y);
+}
+// x (a pair) as three bf16 pairs, each nearest to what the ones before it leave: fp32's 24 bits and exponents.
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    p[i] = pack_bf16x2(x0, x1);
+    x0 -= __uint_as_float(p[i] << 16);
+    x1 -= __uint_as_float(p[i] & 0xffff0000u);
+  }
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -181,7 +201,7 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
   __syncthreads();
   if (warp == 1) G += static_cast<double>(sGh[0]) + static_cast<double>(sGl[0]);
   uint8_t* blob = p.blobs + (static_cast<long>(slot) * d.heads + h) * kDeltaBlob;
-  float* scal = reinterpret_cast<float*>(blob + 2 * kDeltaMat);
+  float* scal = reinterpret_cast<float*>(blob + 3 * kDeltaMat);
   // K K^T and Q K^T of this warp's 16 rows, columns up to its diagonal block; |q|^2 from the diagonal of Q Q^T
   const int gr = lane >> 2, q2 = 2 * (lane & 3);
   float kk[8][4] = {}, qk[8][4] = {}, qq[2][4] = {};
@@ -250,7 +270,7 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
     scal[DS_A * L + tid] = expf(sGh[L - 1]);
   }
   {
-    __nv_bfloat16* P = reinterpret_cast<__nv_bfloat16*>(blob + 2 * kDeltaMat + kDeltaScal);
+    __nv_bfloat16* P = reinterpret_cast<__nv_bfloat16*>(blob + 3 * kDeltaMat + kDeltaScal) + delta_tri_at(warp);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       if (t > 2 * warp + 1) break;
@@ -265,7 +285,7 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
         const float g1 = j + 1 <= i ? expf((hi - gh.y) + (lo - gl.y)) * rk.y : 0.f;
         kk[t][2 * r] = j < i ? bk * g0 * kk[t][2 * r] : 0.f;
         kk[t][2 * r + 1] = j + 1 < i ? bk * g1 * kk[t][2 * r + 1] : 0.f;
-        *reinterpret_cast<uint32_t*>(P + i * kDeltaLd + j) =
+        *reinterpret_cast<uint32_t*>(P + (i & 15) * delta_tri_ld(warp) + j) =
             pack_bf16x2(j <= i ? g0 * rq * qk[t][2 * r] : 0.f, j + 1 <= i ? g1 * rq * qk[t][2 * r + 1] : 0.f);
       }
     }
@@ -321,14 +341,15 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
     constexpr int N = decltype(size)::value, RT = decltype(rows)::value;
     const int o2 = o1 + N, r = (u / (N / 4)) * RT, x = (u % (N / 4)) * 4;
     float y[RT][4];
-    auto product = [&](const float* A, const float* B) {
+    auto product = [&](const float* A, const float* B, auto lower) {  // lower: A's zeros above its diagonal are skipped
 #pragma unroll
       for (int i = 0; i < RT; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
 #pragma unroll 4
-      for (int k = 0; k < N; ++k) {
+      for (int k = 0; k < (decltype(lower)::value ? r + RT : N); ++k) {
         const float4 b = *reinterpret_cast<const float4*>(B + k * 68 + x);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
+          if (decltype(lower)::value && k > r + i) continue;
           const float a = A[(r + i) * 68 + k];
           y[i][0] = fmaf(a, b.x, y[i][0]);
           y[i][1] = fmaf(a, b.y, y[i][1]);
@@ -338,12 +359,12 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
       }
     };
     float* to = sT + o2 * 68 + o1;
-    product(sA + o2 * 68 + o1, sT + o1 * 68 + o1);
+    product(sA + o2 * 68 + o1, sT + o1 * 68 + o1, std::false_type{});
 #pragma unroll
     for (int i = 0; i < RT; ++i)
       *reinterpret_cast<float4*>(to + (r + i) * 68 + x) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
     __syncthreads();
-    product(sT + o2 * 68 + o2, to);
+    product(sT + o2 * 68 + o2, to, std::true_type{});
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -352,26 +373,21 @@ __global__ void __launch_bounds__(128, 5) delta_prep_kernel(const DeltaChunkPara
   };
   merge(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, 32 * (tid >> 6), tid & 63);
   merge(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{}, 0, tid);
-  {
-    const int i = tid >> 1, j0 = (tid & 1) * 32;
-    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(sT[i * 68 + j0 + j] * sB[j0 + j]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    float down, up;
-    pow2_scale(m, down, up);
-    if ((tid & 1) == 0) scal[DS_T * L + i] = up;
-    __half* T = reinterpret_cast<__half*>(blob) + i * kDeltaLd + j0;
+  for (int e = tid; e < L * 8; e += 128) {  // T = inverse diag(beta), 8 values of a row a thread
+    const int i = e >> 3, j = (e & 7) * 8, t = i >> 4;
+    if (j >= 16 * (t + 1)) continue;
+    uint32_t w[4][3];
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        split_f16(sT[i * 68 + j0 + j + 2 * k] * sB[j0 + j + 2 * k] * down,
-                  sT[i * 68 + j0 + j + 2 * k + 1] * sB[j0 + j + 2 * k + 1] * down, hi[k], lo[k]);
-      *reinterpret_cast<uint4*>(T + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(T + L * kDeltaLd + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int k = 0; k < 4; ++k) {
+      const int c = j + 2 * k;
+      const float2 x = *reinterpret_cast<const float2*>(sT + i * 68 + c), b = *reinterpret_cast<const float2*>(sB + c);
+      split_bf16(c <= i ? x.x * b.x : 0.f, c + 1 <= i ? x.y * b.y : 0.f, w[k]);
     }
+    __nv_bfloat16* T = reinterpret_cast<__nv_bfloat16*>(blob) + delta_tri_at(t) + (i & 15) * delta_tri_ld(t) + j;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint4*>(T + k * (kDeltaMat / 2)) = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
   }
 }
 
@@ -495,11 +511,11 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
   for (int c = c0; c < c1; ++c) {
     uint8_t* st = sm + ((c - c0) & 1) * STAGE;
     if (!warp_wait(&full[(c - c0) & 1], ((c - c0) >> 1) & 1, abort_flag, d.status)) break;
-    const uint32_t sK = smem_u32(st), sQ = sK + Cfg::KQ / 2, sT = sK + Cfg::KQ, sP = sT + 2 * kDeltaMat + kDeltaScal;
-    const float* scal = reinterpret_cast<const float*>(st + Cfg::KQ + 2 * kDeltaMat);
+    const uint32_t sK = smem_u32(st), sQ = sK + Cfg::KQ / 2, sT = sK + Cfg::KQ, sP = sT + 3 * kDeltaMat + kDeltaScal;
+    const float* scal = reinterpret_cast<const float*>(st + Cfg::KQ + 3 * kDeltaMat);
     const uint32_t sV = sT + kDeltaBlob + 16 * warp * 2;
 
-    // rows of S^T as fp16 halves; X = K S0, Oi = Q S0 (transposed)
+    // rows of S^T as fp16 halves; X = K S0 (transposed)
     float mx[2] = {0.f, 0.f}, s_dn[2], s_up[2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -514,7 +530,7 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
       }
     };
     row_scale(s_dn, s_up);
-    float X[8][4] = {}, Oi[OUT ? 8 : 1][4] = {};
+    float X[8][4] = {};
 #pragma unroll
     for (int k = 0; k < DK / 16; ++k) {
       uint32_t hi[4], lo[4];
@@ -531,15 +547,9 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
         mma_f16(X[2 * t + 1], hi, b[2], b[3]);
         mma_f16(X[2 * t], lo, b[0], b[1]);
         mma_f16(X[2 * t + 1], lo, b[2], b[3]);
-        if (OUT) {
-          ldsm_x4(sQ + ((16 * t + m_row) * LD + 16 * k + m_col) * 2, b);
-          mma_f16(Oi[OUT ? 2 * t : 0], hi, b[0], b[1]);
-          mma_f16(Oi[OUT ? 2 * t + 1 : 0], hi, b[2], b[3]);
-        }
       }
     }
     // X = V - e^G K^ S0
-    mx[0] = mx[1] = 0.f;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {  // 16 tokens
       uint32_t v[4];
@@ -554,44 +564,97 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
           float(&x)[4] = X[2 * t + u];
           x[2 * r] = fmaf(-x[2 * r], s_up[r] * fx.x, __uint_as_float(w << 16));
           x[2 * r + 1] = fmaf(-x[2 * r + 1], s_up[r] * fx.y, __uint_as_float(w & 0xffff0000u));
-          mx[r] = fmaxf(mx[r], fmaxf(fabsf(x[2 * r]), fabsf(x[2 * r + 1])));
         }
       }
     }
-    float x_dn[2], x_up[2];
-    row_scale(x_dn, x_up);
-    // U = T X
+    // A column's tokens from the first one on that is not finite: cleared for the products, in which it would reach the
+    // tokens before it (0 times it, above the diagonals of T and P), and not finite in what comes out.
+    int cut[2] = {L, L};
+    auto odd = [](const float(&m)[8][4]) {
+      float z[2] = {0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e & 1] = fmaf(m[t][e], 0.f, z[e & 1]);
+      z[0] += z[1];
+      return __any_sync(0xffffffffu, z[0] != z[0]) != 0;
+    };
+    auto clear = [&](float(&m)[8][4]) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!isfinite(m[t][e])) cut[e >> 1] = min(cut[e >> 1], 8 * t + q2 + (e & 1));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        cut[r] = min(cut[r], __shfl_xor_sync(0xffffffffu, cut[r], 1));
+        cut[r] = min(cut[r], __shfl_xor_sync(0xffffffffu, cut[r], 2));
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * t + q2 + (e & 1) >= cut[e >> 1]) m[t][e] = 0.f;
+    };
+    bool bad = odd(X);
+    if (bad) clear(X);
+    // U = T X, both in three bf16 parts: one scale for the column would round small values beside a large one away, of
+    // tokens before it too
     float U[8][4] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint32_t hi[4], lo[4];
+      uint32_t x[3][4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int t = 2 * k + (b >> 1), r = b & 1;
-        split_f16(X[t][2 * r] * x_dn[r], X[t][2 * r + 1] * x_dn[r], hi[b], lo[b]);
+        uint32_t w[3];
+        split_bf16(X[t][2 * r], X[t][2 * r + 1], w);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) x[i][b] = w[i];
       }
 #pragma unroll
-      for (int t = k; t < 4; ++t) {  // rows of T from the diagonal block down
-        uint32_t b[4];
-        ldsm_x4(sT + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
-        mma_f16(U[2 * t], hi, b[0], b[1]);
-        mma_f16(U[2 * t + 1], hi, b[2], b[3]);
-        mma_f16(U[2 * t], lo, b[0], b[1]);
-        mma_f16(U[2 * t + 1], lo, b[2], b[3]);
-        ldsm_x4(sT + kDeltaMat + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
-        mma_f16(U[2 * t], hi, b[0], b[1]);
-        mma_f16(U[2 * t + 1], hi, b[2], b[3]);
-      }
+      for (int t = k; t < 4; ++t)  // rows of T from the diagonal block down
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          uint32_t b[4];
+          ldsm_x4(sT + i * kDeltaMat + (delta_tri_at(t) + m_row * delta_tri_ld(t) + 16 * k + m_col) * 2, b);
+#pragma unroll
+          for (int y = 0; y < 3 - i; ++y) {  // (the products left out are 2^-24 of the whole)
+            mma_bf16(U[2 * t], x[y], b[0], b[1]);
+            mma_bf16(U[2 * t + 1], x[y], b[2], b[3]);
+          }
+        }
     }
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const float2 f = *reinterpret_cast<const float2*>(scal + DS_T * L + 8 * t + q2);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) U[t][e] *= x_up[e >> 1] * (e & 1 ? f.y : f.x);
+    if (bad || odd(U)) {
+      bad = true;
+      clear(U);
     }
     if (OUT) {
-      // O = Q^ S0 e^G + P U, rounded to bf16, through this warp's columns of V's tile
-      float Op[8][4] = {};
+      // O = Q^ S0 e^G + P U, rounded to bf16, through this warp's columns of V's tile (Q S0 only now: beside X and U its
+      // accumulators do not fit into the registers)
+      float O[8][4] = {};
+#pragma unroll
+      for (int k = 0; k < DK / 16; ++k) {
+        uint32_t hi[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int t = 2 * k + (b >> 1), r = b & 1;
+          hi[b] = pack_f16x2(S[t][2 * r] * s_dn[r], S[t][2 * r + 1] * s_dn[r]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t b[4];
+          ldsm_x4(sQ + ((16 * t + m_row) * LD + 16 * k + m_col) * 2, b);
+          mma_f16(O[2 * t], hi, b[0], b[1]);
+          mma_f16(O[2 * t + 1], hi, b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float2 fo = *reinterpret_cast<const float2*>(scal + DS_FO * L + 8 * t + q2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[t][e] *= s_up[e >> 1] * (e & 1 ? fo.y : fo.x);
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t a[4], lo[4];
@@ -605,26 +668,27 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
 #pragma unroll
         for (int t = k; t < 4; ++t) {
           uint32_t b[4];
-          ldsm_x4(sP + ((16 * t + m_row) * kDeltaLd + 16 * k + m_col) * 2, b);
-          mma_bf16(Op[2 * t], a, b[0], b[1]);
-          mma_bf16(Op[2 * t + 1], a, b[2], b[3]);
-          mma_bf16(Op[2 * t], lo, b[0], b[1]);
-          mma_bf16(Op[2 * t + 1], lo, b[2], b[3]);
+          ldsm_x4(sP + (delta_tri_at(t) + m_row * delta_tri_ld(t) + 16 * k + m_col) * 2, b);
+          mma_bf16(O[2 * t], a, b[0], b[1]);
+          mma_bf16(O[2 * t + 1], a, b[2], b[3]);
+          mma_bf16(O[2 * t], lo, b[0], b[1]);
+          mma_bf16(O[2 * t + 1], lo, b[2], b[3]);
         }
+      }
+      if (bad) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * t + q2 + (e & 1) >= cut[e >> 1]) O[t][e] = NAN;
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         uint32_t o[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float2 fo = *reinterpret_cast<const float2*>(scal + DS_FO * L + 16 * t + 8 * u + q2);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float(&a)[4] = Oi[OUT ? 2 * t + u : 0];
-            const float(&b)[4] = Op[2 * t + u];
-            o[2 * u + r] = pack_bf16x2(fmaf(a[2 * r], s_up[r] * fo.x, b[2 * r]),
-                                       fmaf(a[2 * r + 1], s_up[r] * fo.y, b[2 * r + 1]));
-          }
+        for (int b = 0; b < 4; ++b) {
+          const int u = 2 * t + (b >> 1), r = b & 1;
+          o[b] = pack_bf16x2(O[u][2 * r], O[u][2 * r + 1]);
         }
         stsm_x4_t(sV + ((16 * t + (lane & 7) + ((lane >> 4) << 3)) * LDV + ((lane >> 3) & 1) * 8) * 2, o);
       }
@@ -677,6 +741,13 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t + u][e] = fmaf(D[u][e], w_up[e >> 1], a * S[t + u][e]);
+    }
+    if (bad) {  // what is not finite stays in a state
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (cut[e >> 1] < L) S[t][e] = NAN;
     }
     fence_proxy_async_smem();  // (outputs were staged where the next loads go)
     __syncwarp();

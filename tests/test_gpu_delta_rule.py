@@ -343,3 +343,80 @@ def test_rows_of_huge_queries_in_chunks():
     so = torch.zeros_like(state)
     out = op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=so)
     check(out, so, R.delta_rule(q, k, v, g, beta, at, state, 0.125, False), at)
+
+
+LATE = [1e4, 1e6, 1e8, 1e30, float("inf"), -float("inf"), float("nan")]
+
+
+def run_late(op, x, at, state):
+    out, so = torch.zeros_like(x["v"]), torch.zeros_like(state)
+    op.forward(x["q"], x["k"], x["v"], x["g"], x["beta"], ints(at), state_in=state, state_out=so, out=out)
+    assert op.status() == 0
+    return out, so
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", LATE)
+@pytest.mark.parametrize("hq,h,dk,dv,n,t", [(1, 2, 64, 64, 200, 60), (2, 2, 128, 128, 200, 127), (1, 1, 72, 40, 130, 64),
+                                            (1, 2, 128, 128, 1500, 1100)])
+def test_a_value_reaches_no_token_before_it_and_no_other_column(dtype, bad, hq, h, dk, dv, n, t):
+    q, k, v, g, beta = inputs(51, dtype, n, hq, h, dk, dv, rate=0.02)
+    state = torch.randn(1, h, dk, dv, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    x = dict(q=q, k=k, v=v, g=g, beta=beta)
+    op = bd.DeltaRule(hq, h, dk, dv, 1, n, dtype)
+    clean, clean_state = run_late(op, x, [0, n], state)
+    check(clean, clean_state, R.delta_rule(q, k, v, g, beta, [0, n], state, dk ** -0.5, True), [0, n])
+    beta[t, 0] = 0.9
+    clean, clean_state = run_late(op, x, [0, n], state)
+    v[t, 0, 7] = bad
+    out, so = run_late(op, x, [0, n], state)
+    assert torch.equal(out[:t], clean[:t])
+    other = [c for c in range(dv) if c != 7]
+    assert torch.equal(out[:, 0][:, other], clean[:, 0][:, other]) and torch.equal(out[:, 1:], clean[:, 1:])
+    assert torch.equal(so[0, 0][:, other], clean_state[0, 0][:, other]) and torch.equal(so[0, 1:], clean_state[0, 1:])
+    if bad - bad != 0:                                   # and reaches every later token of its column
+        assert (~torch.isfinite(out[t:, 0, 7])).all() and (~torch.isfinite(so[0, 0, :, 7])).all()
+    else:
+        check(out, so, R.delta_rule(q, k, v, g, beta, [0, n], state, dk ** -0.5, True), [0, n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what,bad", [("q", float("nan")), ("q", float("inf")), ("k", float("nan")), ("k", float("inf")),
+                                      ("g", float("nan")), ("beta", float("nan")), ("beta", float("inf"))])
+@pytest.mark.parametrize("t", [0, 5, 17, 40, 47, 63, 64, 100])
+def test_what_is_not_finite_reaches_no_token_before_it(dtype, bad, what, t):
+    n, h = 150, 2
+    q, k, v, g, beta = inputs(52, dtype, n, 1, h, 64, 64, rate=0.02)
+    state = torch.randn(1, h, 64, 64, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    x = dict(q=q, k=k, v=v, g=g, beta=beta)
+    op = bd.DeltaRule(1, h, 64, 64, 1, n, dtype)
+    clean, clean_state = run_late(op, x, [0, n], state)
+    if what in "qk":
+        x[what][t, 0, 9] = bad
+    else:
+        x[what][t, 0] = bad                              # of the first head only
+    out, so = run_late(op, x, [0, n], state)
+    assert torch.equal(out[:t], clean[:t])
+    if what == "q":                                      # one token's output
+        assert torch.equal(out[t + 1:], clean[t + 1:]) and torch.equal(so, clean_state)
+        assert (~torch.isfinite(out[t])).all()
+    else:
+        heads = h if what == "k" else 1
+        assert (~torch.isfinite(out[t:, :heads])).all() and (~torch.isfinite(so[:, :heads])).all()
+        assert torch.equal(out[:, heads:], clean[:, heads:]) and torch.equal(so[:, heads:], clean_state[:, heads:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e3, 1e7, 1e20])
+@pytest.mark.parametrize("t", [0, 3, 8, 40, 70])
+def test_a_large_state_that_is_forgotten_is_gone(dtype, size, t):
+    # tokens behind the one that forgets all are those of a sequence that starts there
+    n, h = 140, 2
+    q, k, v, g, beta = inputs(53, dtype, n, 1, h, 64, 64, rate=0.02)
+    g[t] = -float("inf")
+    state = size * torch.randn(1, h, 64, 64, generator=torch.Generator(device="cuda").manual_seed(7), device="cuda")
+    op = bd.DeltaRule(1, h, 64, 64, 1, n, dtype)
+    out, so = run_late(op, dict(q=q, k=k, v=v, g=g, beta=beta), [0, n], state)
+    # (bounds of a state 0: what was forgotten has no part in them)
+    o, s, ob, sb = R.delta_rule(q[t:], k[t:], v[t:], g[t:], beta[t:], [0, n - t], None, 0.125, True)
+    check(out[t:], so, (o, s, ob, sb), [0, n - t])
