@@ -515,8 +515,10 @@ EDIT_API int edit_packed_attention_forward(const void *q, const void *k, const v
  * d_k a multiple of 8 up to 128, d_v a multiple of 8 up to 256, ldq .. ldo
  * multiples of 8, nseq at most 65535; else EDIT_ERR_UNSUPPORTED.
  * edit_delta_rule_step is one token for each of nseq sequences (row s belongs
- * to sequence s; offsets and rows are not read, no workspace): `state` is
- * updated in place. */
+ * to sequence s; offsets and rows are not read, no workspace and so no status
+ * word): `state` is updated in place. A (sequence, head) whose state did not
+ * arrive on the chip within the time limit of every wait here gets NaN in out,
+ * its state left as it was. */
 typedef struct {
   int dtype; /* edit_dtype of q, k, v, out */
   int qk_heads, heads, d_k, d_v;

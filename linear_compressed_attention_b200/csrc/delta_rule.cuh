@@ -323,10 +323,11 @@ __global__ void __launch_bounds__(128) delta_recurrent_kernel(const DeltaParams 
 // One token of each of many sequences: a block brings a whole (sequence, head)
 // state in with one bulk copy (it is contiguous), keeps its values in registers
 // between the two passes over them and sends it back the same way. A thread has
-// one column and every RS-th row. Bound by the state's bytes, read and written:
-// what matters is how many are under way, three blocks of 64 KB an SM here against
-// 128 KB in the registers of delta_recurrent_kernel (64 sequences x 32 heads of
-// 128 x 128: 55 us against 72).
+// one column and every RS-th row. Bound by the state's bytes, read and written,
+// two blocks of 64 KB an SM (the registers leave room for no third). 64 sequences
+// x 32 heads of 128 x 128: 54 us, delta_recurrent_kernel 72, 16-byte copies by all
+// threads in place of the bulk copy in, whose wait can give up, 60. If it does, the
+// block's out is NaN and its state stays as it was: the call has no status word.
 template <typename T, int DV>
 __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
   pdl_wait();
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
   for (int i = 0; i < 3; ++i) n[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
   const float rk = p.qk_norm ? rsqrtf(n[0] + p.qk_eps) : 1.f;
   const float rq = p.scale * (p.qk_norm ? rsqrtf(n[1] + p.qk_eps) : 1.f);
-  const bool ok = mbar_wait(&full, 0, &abort_flag, nullptr);
+  mbar_wait(&full, 0, &abort_flag, nullptr);
   float S[RPT], r1 = 0.f, r2 = 0.f;
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -391,8 +392,9 @@ __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
     r1 += red[i][0][c];
     r2 += red[i][1][c];
   }
+  const bool lost = *static_cast<volatile int*>(&abort_flag) != 0;  // any thread's wait gave up (it was before the barrier)
   const float u = beta * (v - rk * r1) * rk;  // (times 1/|k|: the state adds k u)
-  if (rg == 0 && ok) static_cast<T*>(p.out)[s * p.ldo + h * DV + c] = from_f32<T>(rq * fmaf(n[2], u, r2));
+  if (rg == 0) static_cast<T*>(p.out)[s * p.ldo + h * DV + c] = from_f32<T>(lost ? NAN : rq * fmaf(n[2], u, r2));
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int r = rg + RS * i;
@@ -400,7 +402,11 @@ __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
   }
   fence_proxy_async_smem();
   __syncthreads();
-  if (tid == 0 && ok) {
+  if (lost) {  // let the copy land before the block exits
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  } else if (tid == 0) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(state), "r"(smem_u32(sS)), "r"(bytes)
                  : "memory");
     bulk_commit();
