@@ -595,6 +595,7 @@ class _Packed:
         self.torch = torch
         self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self.code = EDIT_BF16 if dtype == "bf16" else EDIT_F32
+        self.ran = False
 
     def _workspace(self, nbytes, device):
         if nbytes == 0:
@@ -603,8 +604,9 @@ class _Packed:
         self.args.workspace, self.args.workspace_bytes = self.workspace.data_ptr(), nbytes
 
     def status(self, stream=None) -> int:
-        """The last call's device-side status (EDIT_ERR_SHAPE: offsets or lengths out of range); waits for it."""
-        return edit_attn_read_status(self.workspace, stream)
+        """The last forward call's device-side status (EDIT_ERR_SHAPE: offsets or lengths out of range); waits for it.
+        0 before the first one, which sets the word."""
+        return edit_attn_read_status(self.workspace, stream) if self.ran else 0
 
 
 class PackedAttention(_Packed):
@@ -639,6 +641,7 @@ class PackedAttention(_Packed):
         rc = edit_packed_attention_forward(q, k, v, a, out, stream)
         if rc != 0:
             raise EditError(rc)
+        self.ran = True
         return out
 
 
@@ -688,10 +691,12 @@ class DeltaRule(_Packed):
         rc = edit_delta_rule_forward(q, k, v, g, beta, a, state_in, state_out, out, stream)
         if rc != 0:
             raise EditError(rc)
+        self.ran = True
         return out
 
     def step(self, q, k, v, g, beta, state, out=None, stream=None):
-        """One token of each sequence (row s: sequence s); state is updated in place. Returns out."""
+        """One token of each sequence (row s: sequence s); state is updated in place. Returns out. Has no part in
+        ``status``, which is the last ``forward``'s."""
         n, dev, out = self._inputs(q, k, v, g, beta, out)
         a = self.args
         if n != a.nseq:

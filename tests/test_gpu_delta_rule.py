@@ -420,3 +420,17 @@ def test_a_large_state_that_is_forgotten_is_gone(dtype, size, t):
     # (bounds of a state 0: what was forgotten has no part in them)
     o, s, ob, sb = R.delta_rule(q[t:], k[t:], v[t:], g[t:], beta[t:], [0, n - t], None, 0.125, True)
     check(out[t:], so, (o, s, ob, sb), [0, n - t])
+
+
+def test_status_is_that_of_a_call():
+    # the word lies in memory as it came until a forward call sets it; single tokens have none
+    q, k, v, g, beta = inputs(61, "bf16", 2, 1, 1, 64, 64)
+    op = bd.DeltaRule(1, 1, 64, 64, 2, 2, "bf16")
+    op.workspace.fill_(0x5a)
+    assert op.status() == 0
+    op.step(q, k, v, g, beta, torch.zeros(2, 1, 64, 64, device="cuda"))
+    assert op.status() == 0
+    op.forward(q, k, v, g, beta, ints([0, 2, 1]))
+    assert op.status() == -2
+    op.forward(q, k, v, g, beta, ints([0, 1, 2]))
+    assert op.status() == 0
