@@ -454,6 +454,8 @@ EDIT_API int edit_linear_attention_noalloc(const void *q, const void *k, const v
  *             results of the call are not to be used. Every call sets the word.
  *   Head groups: heads is a multiple of kv_heads (or qk_heads); head h reads
  *             the shared head h / (heads / kv_heads).
+ *   Row counts of attention and the delta rule are at most 2^31 - 512 (else
+ *   EDIT_ERR_UNSUPPORTED); elements are addressed with 64 bits.
  *   Outputs must not overlap the inputs unless a function says so. Tensors of
  *   no rows may be NULL. All memory belongs to the current device, whose SM
  *   count the plans read (query the workspace with that device current). */

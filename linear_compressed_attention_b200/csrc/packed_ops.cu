@@ -61,6 +61,10 @@ int check_ld(int64_t ld, int64_t width) {
   return ld % 8 == 0 ? EDIT_OK : EDIT_ERR_UNSUPPORTED;
 }
 
+// Most rows of a call: row indexes of attention and the delta rule are 32-bit, and
+// their loops step up to a tile (256 rows) past a sequence's end.
+constexpr int64_t kMaxRows = INT32_MAX - 511;
+
 // ------------------------------------------------------------ packed attention
 constexpr size_t kStatusBytes = 256;
 
@@ -89,7 +93,7 @@ int attn_args(const edit_packed_attention* a) {
       a->rows_q < 0 || a->rows_k < 0)
     return EDIT_ERR_SHAPE;
   if (a->d % 8 != 0 || a->d > 128 || a->heads / a->kv_heads > 64 || a->kv_heads > 65535) return EDIT_ERR_UNSUPPORTED;
-  if (a->rows_q > INT32_MAX || a->rows_k > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (a->rows_q > kMaxRows || a->rows_k > kMaxRows) return EDIT_ERR_UNSUPPORTED;
   if (a->rows_q + a->nseq > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
   return EDIT_OK;
 }
@@ -180,7 +184,7 @@ int delta_args(const edit_delta_rule* a, bool step) {
     return EDIT_ERR_SHAPE;
   if (a->d_k % 8 != 0 || a->d_k > 128 || a->d_v % 8 != 0 || a->d_v > 256 || a->heads > 65535)
     return EDIT_ERR_UNSUPPORTED;
-  if (!step && a->rows > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
+  if (!step && a->rows > kMaxRows) return EDIT_ERR_UNSUPPORTED;
   if (static_cast<long>(a->nseq) * 8 * kDeltaMaxSeg > INT32_MAX || (!step && a->nseq > 65535)) return EDIT_ERR_UNSUPPORTED;
   return EDIT_OK;
 }

@@ -192,3 +192,15 @@ def test_dit_block_norms_refused():
     assert call() == UNSUPPORTED
     n.norm_post, n.post_cross_w = 2, 0x6000008
     assert call() == ALIGN
+
+
+@pytest.mark.parametrize("rows", [(1 << 31) - 511, (1 << 31) - 1])
+def test_row_counts_whose_tiles_pass_32_bits_are_refused(rows):
+    # the kernels step in whole tiles: an index past 2^31 - 1 would come back negative
+    assert attn_call(rows_q=rows, dtype=0) == UNSUPPORTED
+    assert attn_call(rows_k=rows, dtype=1) == UNSUPPORTED
+    assert bd.edit_packed_attention_workspace_bytes(attn(rows_q=rows)) == 0
+    assert bd.edit_packed_attention_workspace_bytes(attn(rows_q=(1 << 31) - 512)) > 0
+    assert delta_call(rows=rows) == UNSUPPORTED
+    assert bd.edit_delta_rule_workspace_bytes(delta(rows=rows)) == 0
+    assert bd.edit_delta_rule_workspace_bytes(delta(rows=(1 << 31) - 512)) > 0
