@@ -476,7 +476,7 @@ EDIT_API int edit_linear_attention_noalloc(const void *q, const void *k, const v
  * p_ij to bf16 before the product with v. A NaN or an infinity in k or v
  * reaches the rows that see that key and no others.
  * d a multiple of 8 up to 128, ld* multiples of 8, heads / kv_heads at most 64,
- * scale positive and finite; else EDIT_ERR_UNSUPPORTED. */
+ * scale positive and below 2^127; else EDIT_ERR_UNSUPPORTED. */
 typedef struct {
   int dtype; /* edit_dtype of q, k, v, out */
   int heads, kv_heads, d;

@@ -406,7 +406,8 @@ size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
 int edit_packed_attention_forward(const void* q, const void* k, const void* v, const edit_packed_attention* a,
                                   void* out, void* stream) {
   EDIT_TRY(attn_args(a));
-  if (!(a->scale > 0.f) || std::isinf(a->scale)) return EDIT_ERR_UNSUPPORTED;
+  // (the kernels' exponents are in base 2: scale log2(e), at most twice scale, has to be finite too)
+  if (!(a->scale > 0.f) || std::isinf(2.f * a->scale)) return EDIT_ERR_UNSUPPORTED;
   if (!a->q_offsets || !a->k_offsets || !a->workspace) return EDIT_ERR_NULL;
   if (a->rows_q > 0 && (!q || !out)) return EDIT_ERR_NULL;
   if (a->rows_k > 0 && (!k || !v)) return EDIT_ERR_NULL;

@@ -204,3 +204,8 @@ def test_row_counts_whose_tiles_pass_32_bits_are_refused(rows):
     assert delta_call(rows=rows) == UNSUPPORTED
     assert bd.edit_delta_rule_workspace_bytes(delta(rows=rows)) == 0
     assert bd.edit_delta_rule_workspace_bytes(delta(rows=(1 << 31) - 512)) > 0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, 3e38])
+def test_scales_that_are_infinite_in_base_2_are_refused(scale):
+    assert attn_call(scale=scale) == UNSUPPORTED
