@@ -476,6 +476,9 @@ class DitBlock:
 
     def __init__(self, arrays: dict, B: int, H: int, W: int, N_T: int, C: int, heads: int, dtype: str = "bf16",
                  device="cuda", side: bool = True, norms: tuple | None = None):
+        for n, a in (norms[2] if norms is not None and len(norms) > 2 else {}).items():
+            if n not in DIT_NORM_WEIGHTS or np.shape(a) != (C,):
+                raise ValueError(f"norm weight {n}: one of {DIT_NORM_WEIGHTS} of shape ({C},) expected")
         import torch
         self.torch = torch
         self.B, self.H, self.W, self.N_T, self.C, self.heads = B, H, W, N_T, C, heads

@@ -2,6 +2,7 @@
 documented codes, before touching the device (no GPU here)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -209,3 +210,11 @@ def test_row_counts_whose_tiles_pass_32_bits_are_refused(rows):
 @pytest.mark.parametrize("scale", [2.0 ** 127, 3e38])
 def test_scales_that_are_infinite_in_base_2_are_refused(scale):
     assert attn_call(scale=scale) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("weights", [dict(post_atn_w=np.ones(1152)), dict(post_ffn_w=np.ones(576)),
+                                     dict(pre_attn_w=np.ones((2, 576)))])
+def test_dit_block_norm_weights_of_another_name_or_shape_are_refused(weights):
+    # a misspelt weight would be left out, a short one read past its end
+    with pytest.raises(ValueError, match="norm weight"):
+        bd.DitBlock({}, 1, 64, 64, 300, 1152, 16, norms=("layer", "rms", weights))
