@@ -605,6 +605,13 @@ class _Packed:
             raise ValueError("shape/dtype rejected by the workspace query")
         self.workspace = self.torch.empty(nbytes, dtype=self.torch.uint8, device=device)
         self.args.workspace, self.args.workspace_bytes = self.workspace.data_ptr(), nbytes
+        self.device = self.workspace.get_device()
+
+    def _current_device(self):
+        dev = self.torch.cuda.current_device()
+        if dev != self.device:
+            raise ValueError(f"the workspace is on device {self.device}, the current device is {dev}")
+        return dev
 
     def status(self, stream=None) -> int:
         """The last forward call's device-side status (EDIT_ERR_SHAPE: offsets or lengths out of range); waits for it.
@@ -629,7 +636,7 @@ class PackedAttention(_Packed):
 
     def forward(self, q, k, v, q_offsets, k_offsets, k_lens=None, out=None, stream=None):
         """q [rows, heads, d], k, v [rows, kv_heads, d]; int32 device offsets [nseq + 1] and lengths [nseq]."""
-        a, dev = self.args, self.torch.cuda.current_device()
+        a, dev = self.args, self._current_device()
         rk = k.shape[0]
         a.rows_q, a.rows_k = q.shape[0], rk
         a.ldq = _check_rows("q", q, self.tdtype, (a.rows_q, a.heads, a.d), dev)
@@ -665,7 +672,7 @@ class DeltaRule(_Packed):
         self._workspace(edit_delta_rule_workspace_bytes(a), device)
 
     def _inputs(self, q, k, v, g, beta, out):
-        a, dev, f32 = self.args, self.torch.cuda.current_device(), self.torch.float32
+        a, dev, f32 = self.args, self._current_device(), self.torch.float32
         n = q.shape[0]
         a.ldq = _check_rows("q", q, self.tdtype, (n, a.qk_heads, a.d_k), dev)
         a.ldk = _check_rows("k", k, self.tdtype, (n, a.qk_heads, a.d_k), dev)
@@ -733,12 +740,15 @@ class BlockNorm:
                 if t.dtype != self.tdtype or tuple(t.shape) != (C,) or not t.is_contiguous() or not t.is_cuda:
                     raise ValueError(f"{n}: contiguous {self.tdtype} ({C},) on the device expected")
                 setattr(a, n, t.data_ptr())
+        self.devices = {t.get_device() for t in self.kept.values() if t is not None}  # of the kept vectors
 
     def forward(self, x, y=None, gate=None, scale=None, shift=None, offsets=None, r_out=None, h_out=None,
                 want_r: bool = True, want_h: bool = True, stream=None):
         """x, y [rows, C]; gate, scale, shift [samples, C] with one row stride; int32 device offsets [samples + 1],
         or equal shares of the rows without them. Returns (r, h), None for one that is not wanted."""
         a, dev = self.args, self.torch.cuda.current_device()
+        if self.devices and self.devices != {dev}:
+            raise ValueError(f"the kept vectors are on devices {self.devices}, the current device is {dev}")
         n, C = x.shape[0], a.C
         a.rows = n
         a.ldx = _check_rows("x", x, self.tdtype, (n, C), dev)

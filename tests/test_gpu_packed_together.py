@@ -102,3 +102,24 @@ def test_prompts_then_tokens(dtype):
     st.forward(torch.randn(7, 256, generator=g, device="cuda").to(st.dt), gate, [3, 4, 0], False)   # prompts go on
     for _ in range(3):
         st.forward(torch.randn(3, 256, generator=g, device="cuda").to(st.dt), gate, [1, 1, 1], True)
+
+
+def test_objects_are_used_on_their_own_device(monkeypatch):
+    # a workspace or kept weights of another device: refused, with every other tensor where it should be (one device is
+    # visible here: the object is told that its memory lies on the next one)
+    attn = bd.PackedAttention(2, 2, 64, 1, 4, 4, "bf16")
+    delta = bd.DeltaRule(2, 2, 64, 64, 1, 4, "bf16")
+    norm = bd.BlockNorm(64, "bf16", pre_w=torch.ones(64, device="cuda", dtype=torch.bfloat16))
+    at = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    x = torch.ones(4, 2, 64, device="cuda", dtype=torch.bfloat16)
+    z = torch.zeros(4, 2, device="cuda")
+    state = torch.zeros(1, 2, 64, 64, device="cuda")
+    calls = [(attn, lambda: attn.forward(x, x, x, at, at)), (delta, lambda: delta.forward(x, x, x, z, z, at)),
+             (delta, lambda: delta.step(x[:1], x[:1], x[:1], z[:1], z[:1], state)), (norm, lambda: norm.forward(x[:, 0]))]
+    for op, call in calls:
+        call()
+        name = "devices" if op is norm else "device"
+        with monkeypatch.context() as m:
+            m.setattr(op, name, {1} if op is norm else 1)
+            with pytest.raises(ValueError, match="device"):
+                call()
