@@ -328,10 +328,12 @@ __global__ void __launch_bounds__(128) delta_recurrent_kernel(const DeltaParams 
 // x 32 heads of 128 x 128: 54 us, delta_recurrent_kernel 72, 16-byte copies by all
 // threads in place of the bulk copy in, whose wait can give up, 60. If it does, the
 // block's out is NaN and its state stays as it was: the call has no status word.
-template <typename T, int DV>
+constexpr int kDeltaStepDv = 128;
+
+template <typename T>
 __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
   pdl_wait();
-  constexpr int RS = 256 / DV, RPT = 128 / RS;  // row groups; rows a thread at most
+  constexpr int DV = kDeltaStepDv, RS = 256 / DV, RPT = 128 / RS;  // row groups; rows a thread at most
   extern __shared__ __align__(128) uint8_t dsm[];
   float* sS = reinterpret_cast<float*>(dsm);  // [d_k][DV]
   __shared__ float sk[128], sq[128], part[8][3], red[RS][2][DV];

@@ -247,9 +247,9 @@ int delta_recurrent(const DeltaParams& p, cudaStream_t st) {
 template <typename T>
 int delta_single(const DeltaParams& p, cudaStream_t st) {
   const long blocks = static_cast<long>(p.nseq) * p.heads;
-  if (p.d_v == 128 && 4 * blocks >= 3L * device_sms())
-    return launch(delta_step_kernel<T, 128>, dim3(static_cast<unsigned>(p.nseq), p.heads), dim3(256),
-                  static_cast<size_t>(p.d_k) * 128 * 4, st, p);
+  if (p.d_v == kDeltaStepDv && 4 * blocks >= 3L * device_sms())
+    return launch(delta_step_kernel<T>, dim3(static_cast<unsigned>(p.nseq), p.heads), dim3(256),
+                  static_cast<size_t>(p.d_k) * kDeltaStepDv * 4, st, p);
   return delta_recurrent<T, true>(p, st);
 }
 
@@ -367,14 +367,13 @@ int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
   if (p.rows > 2L * device_sms()) {
     if (nv <= 32) return norm_rows<T, 8, 32, 1>(p, st);
     if (nv <= 64) return norm_rows<T, 8, 32, 2>(p, st);
-    if (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
       if (nv <= 96) return norm_rows<T, 8, 32, 3>(p, st);
       if (nv <= 128) return norm_rows<T, 8, 32, 4>(p, st);
       if (nv <= 160) return norm_rows<T, 8, 32, 5>(p, st);
+      return nv <= 192 ? norm_rows<T, 8, 64, 3>(p, st) : norm_rows<T, 8, 64, 4>(p, st);
     }
   }
-  if (sizeof(T) == 2 && nv > 160 && p.rows > 2L * device_sms())
-    return nv <= 192 ? norm_rows<T, 8, 64, 3>(p, st) : norm_rows<T, 8, 64, 4>(p, st);
   return nv <= 128 ? norm_rows<T, 8, 128, 1>(p, st) : norm_rows<T, 8, 128, 2>(p, st);
 }
 
