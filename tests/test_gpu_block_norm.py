@@ -177,3 +177,37 @@ def test_one_sample_a_row():
                        dict(gate=m, scale=m, shift=m))
     check(r, ref[0], ref[2])
     check(h, ref[1], ref[3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("rows", [37, 700])
+@pytest.mark.parametrize("C", [64, 1001, 1152, 3000])
+def test_values_that_are_not_finite_stay_in_their_row_or_sample(dtype, bad, rows, C):
+    x, y = rand(61, dtype, rows, C), rand(62, dtype, rows, C)
+    mod = rand(63, dtype, 3, 3, C)
+    at = ints([0, 5, 20, rows])
+    op = bd.BlockNorm(C, dtype, post="rms", pre="layer")
+
+    def run():
+        return op.forward(x, y, gate=mod[:, 0], scale=mod[:, 1], shift=mod[:, 2], offsets=at)
+    clean = run()
+    for t in (x, y):                                     # one row: the norm before the next branch spreads it over the row
+        was = t[7, 3].clone()
+        t[7, 3] = bad
+        r, h = run()
+        t[7, 3] = was
+        others = [i for i in range(rows) if i != 7]
+        assert torch.equal(r[others], clean[0][others]) and torch.equal(h[others], clean[1][others])
+        assert not torch.isfinite(r[7, 3]) and torch.isnan(h[7]).all()
+    for i in range(3):                                   # one value of one sample's gate, scale, shift
+        was = mod[1, i, 3].clone()
+        mod[1, i, 3] = bad
+        r, h = run()
+        mod[1, i, 3] = was
+        others = [i for i in range(rows) if not 5 <= i < 20]
+        assert torch.equal(r[others], clean[0][others]) and torch.equal(h[others], clean[1][others])
+        assert (~torch.isfinite((r if i == 0 else h)[5:20, 3])).all()
+        if i:                                            # that column only
+            cols = [c for c in range(C) if c != 3]
+            assert torch.equal(r, clean[0]) and torch.equal(h[5:20][:, cols], clean[1][5:20][:, cols])

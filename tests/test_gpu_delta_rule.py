@@ -434,3 +434,52 @@ def test_status_is_that_of_a_call():
     assert op.status() == -2
     op.forward(q, k, v, g, beta, ints([0, 1, 2]))
     assert op.status() == 0
+
+
+def final_states(k, v, g, beta, at, state):
+    """The final states in 64 bits and, per (sequence, head), the largest norm a state had on the way."""
+    H, dk, dv = v.shape[1], k.shape[2], v.shape[2]
+    kd = k.double() / (k.double().square().sum(-1, keepdim=True) + 1e-6).sqrt()
+    kd, a, b, vd = kd.repeat_interleave(H // k.shape[1], 1), g.double().exp(), beta.double(), v.double()
+    S, most = state.double().clone(), state.double().flatten(2).norm(dim=-1)
+    for s in range(len(at) - 1):
+        for t in range(at[s], at[s + 1]):
+            S[s] *= a[t][:, None, None]
+            u = b[t][:, None] * (vd[t] - torch.einsum("hk,hkv->hv", kd[t], S[s]))
+            S[s] += kd[t][:, :, None] * u[:, None, :]
+            most[s] = torch.maximum(most[s], S[s].flatten(1).norm(dim=-1))
+    return S, most
+
+
+@pytest.mark.parametrize("hq,h,dk,dv,lens", [(1, 2, 64, 64, [64]), (1, 2, 128, 128, [128, 70]), (2, 2, 72, 40, [200]),
+                                             (1, 4, 128, 128, [1500])])
+def test_states_of_chunks_keep_fp32_precision(hq, h, dk, dv, lens):
+    # A chunk's three products each see an operand off by 2^-23 of its column's largest value, some 4.5 times the
+    # column's mean size: 4.5 sqrt(3) 2^-23 = 9e-7 in norm, the roundings being independent; fp32 sums of up to 200 terms
+    # add sqrt(200) 2^-24 = 8e-7; the triangular inverse of nearly orthogonal keys at most doubles it: 4e-6 of the
+    # largest state for each chunk. An operand without its low half is off by 2^-12 of each value, 1e-4 in norm.
+    at = offsets(lens)
+    q, k, v, g, beta = inputs(71, "bf16", at[-1], hq, h, dk, dv, rate=0.01)
+    state = torch.randn(len(lens), h, dk, dv, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda")
+    op = bd.DeltaRule(hq, h, dk, dv, len(lens), at[-1], "bf16")
+    so = torch.zeros_like(state)
+    op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=so)
+    ref, most = final_states(k, v, g, beta, at, state)
+    chunks = torch.tensor([-(-n // 64) for n in lens], device="cuda")[:, None]
+    e = (so.double() - ref).flatten(2).norm(dim=-1)
+    assert (e <= 4e-6 * chunks * most).all(), float((e / most).max())
+
+
+@pytest.mark.parametrize("S,h,lens", [(2, 20, [1500, 1100]), (1, 40, [2100])])
+def test_parts_of_many_heads_match_the_64_bit_form(S, h, lens):
+    # more blocks than SMs in each pass over the parts: some heads of the first and of the last blocks
+    at = offsets(lens)
+    q, k, v, g, beta = inputs(72, "bf16", at[-1], h // 2, h, 128, 128, rate=0.02)
+    state = torch.randn(S, h, 128, 128, generator=torch.Generator(device="cuda").manual_seed(9), device="cuda")
+    op = bd.DeltaRule(h // 2, h, 128, 128, S, at[-1], "bf16")
+    so = torch.zeros_like(state)
+    out = op.forward(q, k, v, g, beta, ints(at), state_in=state, state_out=so)
+    some = [0, h // 2, h - 2, h - 1]
+    of = [i // 2 for i in some]
+    ref = R.delta_rule(q[:, of], k[:, of], v[:, some], g[:, some], beta[:, some], at, state[:, some], 128 ** -0.5, True)
+    check(out[:, some], so[:, some], ref, at)
