@@ -568,23 +568,23 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
       }
     }
     // A column's tokens from the first one on that is not finite: cleared for the products, in which it would reach the
-    // tokens before it (0 times it, above the diagonals of T and P), and not finite in what comes out.
+    // tokens before it (0 times it, above the diagonals of T and P), and not finite in what comes out. From 2^128 - 2^119
+    // on a value is infinite in bf16 and counts as such.
     int cut[2] = {L, L};
     auto odd = [](const float(&m)[8][4]) {
       float z[2] = {0.f, 0.f};
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e & 1] = fmaf(m[t][e], 0.f, z[e & 1]);
-      z[0] += z[1];
-      return __any_sync(0xffffffffu, z[0] != z[0]) != 0;
+        for (int e = 0; e < 4; ++e) z[e & 1] = fmaf(m[t][e], 4.f, z[e & 1]);
+      return __any_sync(0xffffffffu, !(fabsf(z[0]) < INFINITY && fabsf(z[1]) < INFINITY)) != 0;  // (or sums past 2^128)
     };
     auto clear = [&](float(&m)[8][4]) {
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (!isfinite(m[t][e])) cut[e >> 1] = min(cut[e >> 1], 8 * t + q2 + (e & 1));
+          if (!(fabsf(m[t][e]) < 0x1.ffp127f)) cut[e >> 1] = min(cut[e >> 1], 8 * t + q2 + (e & 1));
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         cut[r] = min(cut[r], __shfl_xor_sync(0xffffffffu, cut[r], 1));

@@ -483,3 +483,20 @@ def test_parts_of_many_heads_match_the_64_bit_form(S, h, lens):
     of = [i // 2 for i in some]
     ref = R.delta_rule(q[:, of], k[:, of], v[:, some], g[:, some], beta[:, some], at, state[:, some], 128 ** -0.5, True)
     check(out[:, some], so[:, some], ref, at)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("size", [0.0, 3e36])
+def test_values_at_the_end_of_the_range_reach_no_token_before_them(sign, size):
+    # the largest bf16 value, and what a state makes of it: finite in fp32 and past the largest bf16 value
+    n, h, t = 64, 2, 40
+    q, k, v, g, beta = inputs(54, "bf16", n, 1, h, 64, 64, rate=0.001)
+    state = size * torch.randn(1, h, 64, 64, generator=torch.Generator(device="cuda").manual_seed(10), device="cuda")
+    op = bd.DeltaRule(1, h, 64, 64, 1, n, "bf16")
+    x = dict(q=q, k=k, v=v, g=g, beta=beta)
+    clean, _ = run_late(op, x, [0, n], state)
+    assert torch.isfinite(clean).all()
+    v[t, 0, ::2] = sign * torch.finfo(torch.bfloat16).max
+    out, _ = run_late(op, x, [0, n], state)
+    assert torch.equal(out[:t], clean[:t]) and torch.equal(out[:, :, 1::2], clean[:, :, 1::2])
+    assert torch.equal(out[:, 1:], clean[:, 1:])
