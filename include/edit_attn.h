@@ -514,6 +514,14 @@ EDIT_API int edit_packed_attention_forward(const void *q, const void *k, const v
  * state_in NULL starts from zeros, state_out NULL drops the final states; the
  * two may be the same buffer (not overlap in another way). A sequence of no rows
  * copies its state.
+ * Sums and states are fp32. bf16 calls of edit_delta_rule_forward with 32 rows a
+ * sequence or more on average run in chunks of 64 tokens: states are then within
+ * some 2^-22 of the largest value of their columns (v's index) a chunk, and o_t,
+ * besides its own rounding, within some 2^-11 of scale |q_t| times that value and
+ * 2^-9 of each of the chunk's own terms. A token's results depend on no later token,
+ * and a column's on no other column of v: a value that is not finite (from
+ * 2^128 - 2^119 on in chunks) makes the results of its token and the later ones not
+ * finite, as NaN in chunks, in v of that column and in k, g, beta of all.
  * d_k a multiple of 8 up to 128, d_v a multiple of 8 up to 256, ldq .. ldo
  * multiples of 8, nseq at most 65535; else EDIT_ERR_UNSUPPORTED.
  * edit_delta_rule_step is one token for each of nseq sequences (row s belongs

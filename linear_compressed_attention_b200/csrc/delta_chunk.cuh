@@ -15,9 +15,11 @@
 // next product (mma.sync m16n8k16), and the whole chain of a chunk needs no
 // shared memory between its products and no block-wide wait. (The chain is three
 // dependent products of 16 x 64 x 128 and less for each warp: too small and too
-// serial for tcgen05's 128-row tiles to pay.) 8192 tokens of 16 heads of 128 take 341
-// us in 9 parts: inverses 67, effects of the parts 152, join 36, walk 112; the walks
-// are bound by mma.sync and its operands' splitting, about 5 us a chunk of 8 warps.
+// serial for tcgen05's 128-row tiles to pay; whole heads on one tile are not.) 8192
+// tokens of 16 heads of 128 take 357 us in 9 parts; profiled one by one, with cold
+// caches, inverses 63, effects of the parts 164, join 36, walk 119. The walks are bound
+// by mma.sync and its operands' splitting (tensor pipe half busy), 6.7 us a chunk of 8
+// warps.
 //
 // Precision: the state is fp32. Its products take fp16 operands: a column of the
 // state (of the decayed U in the state's sum) is scaled by a power of two to
@@ -29,7 +31,7 @@
 // of each term: there the tokens of a chunk meet, and with one scale for all of them
 // a large value, even of a later token or of a state since forgotten, rounded small
 // ones away (with three products of fp16 halves the walks were 5% shorter). O is
-// rounded to bf16, so Q^ S0 takes one fp16 half, 2^-12 of the column's largest value
+// rounded to bf16, so Q^ S0 takes one fp16 half, 2^-11 of the column's largest value
 // for each term, and P U, whose terms a decay may set many powers of two apart, P in
 // bf16 and U in two bf16 halves (with U in one, O was 1.5 times as far off as its own
 // rounding).

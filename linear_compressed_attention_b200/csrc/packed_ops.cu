@@ -255,8 +255,8 @@ int delta_single(const DeltaParams& p, cudaStream_t st) {
 
 // bf16 calls with sequences of at least this many rows on average run in chunks
 // of 64 tokens, others token by token (16 heads of 128, us for 64 sequences of 16 /
-// 32 / 64 tokens: 133 / 136 / 140 in chunks, 96 / 163 / 298 token by token; one
-// sequence: 22 / 22 / 23 and 9 / 15 / 28).
+// 32 / 64 tokens: 117 / 121 / 129 in chunks, 88 / 156 / 291 token by token; one
+// sequence: 22 / 22 / 23 and 12 / 16 / 28).
 constexpr int kDeltaChunkedRows = 32;
 
 struct DeltaPlan {
@@ -269,8 +269,10 @@ struct DeltaPlan {
 // walk over the chunks leaves SMs idle. A part's effect is found first (pass 1,
 // on d_v + d_k columns), the effects are joined part after part, then the parts
 // run side by side (pass 2). The number with the least time, in chunks of pass 2
-// (measured: a chunk of pass 1 takes 0.87, a join 1.5; 8192 tokens of 16 heads of
-// 128: 842 us in one part, 448 in 4, 386 in 5, 358 in 9, 406 in 16).
+// (a chunk of pass 1 counts 0.87, a join 1.5; 8192 tokens of 16 heads of 128: 927 us
+// in one part, 463 in 4, 397 in 5, 358 in 9, 418 in 16; 4096 tokens of 4 heads: 446,
+// 223, 193, 145, 130, where it takes 8 parts, 146; 1500 and 1100 tokens of 20 heads of
+// 128: 199 in one, 198 in 3, 217 in 4). It knows the mean length only.
 int delta_nseg(const edit_delta_rule* a, int64_t chunks, int sms) {
   const int64_t heads = static_cast<int64_t>(a->nseq) * a->heads;
   const int64_t b1 = heads * ceil_div(a->d_v + a->d_k, kDeltaCols), b2 = heads * ceil_div(a->d_v, kDeltaCols);
