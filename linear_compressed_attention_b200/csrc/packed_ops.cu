@@ -86,14 +86,14 @@ int attn_rows(const edit_packed_attention* a, int64_t rows) {
   return a->dtype == EDIT_BF16 ? attn_row_tiles(a, rows) * (128 / G) : 64 / G;
 }
 
-int attn_args(const edit_packed_attention* a) {
+int attn_args(const edit_packed_attention* a, bool query) {  // query: what the workspace depends on
   if (!a) return EDIT_ERR_NULL;
   if (a->dtype != EDIT_F32 && a->dtype != EDIT_BF16) return EDIT_ERR_DTYPE;
   if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0 || a->d < 1 || a->nseq < 1 || a->max_k < 0 ||
-      a->rows_q < 0 || a->rows_k < 0)
+      a->rows_q < 0 || (!query && a->rows_k < 0))
     return EDIT_ERR_SHAPE;
   if (a->d % 8 != 0 || a->d > 128 || a->heads / a->kv_heads > 64 || a->kv_heads > 65535) return EDIT_ERR_UNSUPPORTED;
-  if (a->rows_q > kMaxRows || a->rows_k > kMaxRows) return EDIT_ERR_UNSUPPORTED;
+  if (a->rows_q > kMaxRows || (!query && a->rows_k > kMaxRows)) return EDIT_ERR_UNSUPPORTED;
   if (a->rows_q + a->nseq > INT32_MAX) return EDIT_ERR_UNSUPPORTED;
   return EDIT_OK;
 }
@@ -384,7 +384,7 @@ int norm_run(const BlockNormParams& p, bool vec, cudaStream_t st) {
 extern "C" {
 
 size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
-  if (attn_args(a) != EDIT_OK) return 0;
+  if (attn_args(a, true) != EDIT_OK) return 0;
   // Fewer rows can mean more parts: the most over all row counts up to rows_q and
   // both tile heights. Rows with the same number of slots have the same parts, so
   // the last of each are enough, and more slots never have more parts (no rows at
@@ -406,7 +406,7 @@ size_t edit_packed_attention_workspace_bytes(const edit_packed_attention* a) {
 
 int edit_packed_attention_forward(const void* q, const void* k, const void* v, const edit_packed_attention* a,
                                   void* out, void* stream) {
-  EDIT_TRY(attn_args(a));
+  EDIT_TRY(attn_args(a, false));
   // (the kernels' exponents are in base 2: scale log2(e), at most twice scale, has to be finite too)
   if (!(a->scale > 0.f) || std::isinf(2.f * a->scale)) return EDIT_ERR_UNSUPPORTED;
   if (!a->q_offsets || !a->k_offsets || !a->workspace) return EDIT_ERR_NULL;

@@ -218,3 +218,10 @@ def test_dit_block_norm_weights_of_another_name_or_shape_are_refused(weights):
     # a misspelt weight would be left out, a short one read past its end
     with pytest.raises(ValueError, match="norm weight"):
         bd.DitBlock({}, 1, 64, 64, 300, 1152, 16, norms=("layer", "rms", weights))
+
+
+@pytest.mark.parametrize("rows_k", [-5, 0, 1 << 40])
+def test_attention_workspace_query_does_not_read_the_keys(rows_k):
+    # a caller sizes the workspace before it knows how many rows its cache will have
+    assert bd.edit_packed_attention_workspace_bytes(attn(rows_k=rows_k)) == \
+        bd.edit_packed_attention_workspace_bytes(attn()) > 0
