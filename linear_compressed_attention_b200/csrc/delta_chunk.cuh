@@ -461,7 +461,10 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
     for (int c = c0; c < c1; ++c) {
       uint8_t* st = sm + ((c - c0) & 1) * STAGE;
       uint64_t* bar = &full[(c - c0) & 1];
-      if (!warp_wait(&empty[(c - c0) & 1], (((c - c0) >> 1) & 1) ^ 1, abort_flag, d.status)) break;
+      if (!warp_wait(&empty[(c - c0) & 1], (((c - c0) >> 1) & 1) ^ 1, abort_flag, d.status)) {
+        let_copies_land();
+        break;
+      }
       const int n = min(L, sr.len - c * L);
       __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(st + Cfg::KQ + kDeltaBlob);
       for (int r = n; r < L; ++r)  // rows behind the sequence: zeros
@@ -512,7 +515,10 @@ __global__ void __launch_bounds__(288, 1) delta_chunk_kernel(const DeltaChunkPar
   const int t_row = lane & 15, t_col = (lane >> 4) * 8;                              // (k, n) blocks, transposed
   for (int c = c0; c < c1; ++c) {
     uint8_t* st = sm + ((c - c0) & 1) * STAGE;
-    if (!warp_wait(&full[(c - c0) & 1], ((c - c0) >> 1) & 1, abort_flag, d.status)) break;
+    if (!warp_wait(&full[(c - c0) & 1], ((c - c0) >> 1) & 1, abort_flag, d.status)) {
+      let_copies_land();
+      break;
+    }
     const uint32_t sK = smem_u32(st), sQ = sK + Cfg::KQ / 2, sT = sK + Cfg::KQ, sP = sT + 3 * kDeltaMat + kDeltaScal;
     const float* scal = reinterpret_cast<const float*>(st + Cfg::KQ + 3 * kDeltaMat);
     const uint32_t sV = sT + kDeltaBlob + 16 * warp * 2;

@@ -404,10 +404,8 @@ __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
   }
   fence_proxy_async_smem();
   __syncthreads();
-  if (lost) {  // let the copy land before the block exits
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 2000000ull) {
-    }
+  if (lost) {
+    let_copies_land();
   } else if (tid == 0) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(state), "r"(smem_u32(sS)), "r"(bytes)
                  : "memory");

@@ -270,11 +270,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
         }
         ok = __all_sync(0xffffffffu, ok);
       }
-      if (lane == 0 && *abort_flag) {  // let copies already issued land before the block exits
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) {
-        }
-      }
+      if (lane == 0 && *abort_flag) let_copies_land();
     } else if (warp == W_MMA) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t tmem = *tmem_slot;

@@ -10,6 +10,14 @@ namespace edit {
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
+// After a wait that gave up: time for the copies this block has under way, which
+// must not land in the shared memory of a block after it.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000ull) {
+  }
+}
+
 struct SeqRows {
   int begin, len;
 };
